@@ -17,3 +17,5 @@ from ._binding import (GdnError, GdnOptions, GdnTensor, GdnWorkspaceLayout,  # n
                        gdn_status_string, gdn_workspace_size, library_path,
                        options)
 from ._binding import GraphCache, PreparedPrefill  # noqa: F401,E402
+from ._layer import (GdnSsmOptions, gdn_add_rms_norm, gdn_short_conv, gdn_ssm_decode,  # noqa: F401,E402
+                     gdn_ssm_default_options, gdn_ssm_prefill, gdn_ssm_workspace_size, ssm_workspace)

@@ -17,7 +17,7 @@ import torch
 GDN_OK = 0
 # The C ABI these structures and prototypes describe (GDN_ABI_VERSION of
 # include/gdn.h); a library built from other sources is refused at load.
-ABI_VERSION = 9
+ABI_VERSION = 10
 STATUS_NAMES = {0: "GDN_OK", -1: "GDN_ERR_NULL_ARG", -2: "GDN_ERR_DTYPE",
                 -3: "GDN_ERR_SHAPE", -4: "GDN_ERR_LAYOUT",
                 -5: "GDN_ERR_UNSUPPORTED", -6: "GDN_ERR_WORKSPACE",
@@ -29,7 +29,8 @@ EXPORTED = ("gdn_abi_version", "gdn_default_options", "gdn_prefill",
             "gdn_prefill_ex", "gdn_prefill_noalloc", "gdn_workspace_size", "gdn_get_workspace_layout",
             "gdn_decode", "gdn_output_gate", "gdn_check_cu_seqlens", "gdn_graph_cache_create", "gdn_graph_cache_destroy",
             "gdn_graph_cache_clear", "gdn_graph_cache_stats", "gdn_prefill_graph",
-            "gdn_status_string", "gdn_last_error")
+            "gdn_short_conv", "gdn_ssm_default_options", "gdn_ssm_prefill", "gdn_ssm_workspace_size",
+            "gdn_ssm_decode", "gdn_add_rms_norm", "gdn_status_string", "gdn_last_error")
 
 _DTYPES = {torch.bfloat16: 1, torch.float32: 2, torch.int32: 3, torch.int64: 4}
 

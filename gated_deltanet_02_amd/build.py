@@ -1,7 +1,8 @@
 """Build the gfx950 library ``libgdn.so`` next to this file with hipcc.
 
-Sources: csrc/gdn_kernels.hip (kernels, device code) and csrc/gdn_api.cpp
-(the C ABI declared in include/gdn.h).  Compiled for gfx950 only, with packed
+Sources: csrc/*.hip (kernels, device code: the delta rule, the operators
+around a layer's projections, the state space scan) and csrc/*_api.cpp (the
+C ABI declared in include/gdn.h).  Compiled for gfx950 only, with packed
 fp32 VALU instructions disabled.
 """
 from __future__ import annotations
@@ -28,7 +29,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-mllvm", "-amdgpu-mfma-vgpr-form",
           f"-I{INCLUDE}", f"-I{CSRC}"]
-SOURCES = ["gdn_kernels.hip", "gdn_api.cpp"]
+SOURCES = ["gdn_kernels.hip", "gdn_layer.hip", "gdn_ssm.hip", "gdn_api.cpp", "gdn_layer_api.cpp"]
 
 
 def build(verbose: bool = False) -> str:

@@ -18,6 +18,7 @@
 #include <string>
 
 #include "gdn.h"
+#include "gdn_api_common.h"
 #include "gdn_cu_check.h"
 #include "gdn_internal.h"
 #include "gdn_launch.h"
@@ -26,16 +27,35 @@ namespace {
 
 thread_local std::string g_last_error;
 
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int status, const char* fmt, ...) {
+int vfail(int status, const char* fmt, va_list ap) {
   char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
   vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
   g_last_error = buf;
   return status;
 }
+
+int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int fail(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vfail(status, fmt, ap);
+  va_end(ap);
+  return status;
+}
+
+}  // namespace
+
+int gdn::api_fail(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vfail(status, fmt, ap);
+  va_end(ap);
+  return status;
+}
+
+void gdn::api_clear_error() { g_last_error.clear(); }
+
+namespace {
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -540,14 +560,14 @@ bool debug_check_enabled() {
 
 // GDN_DEBUG_CHECK=1: the device table is checked before anything else is
 // enqueued (skipped while the stream is being captured).
-int debug_check_cu(const Problem& P, const gdn_tensor* cu, hipStream_t s) {
+int debug_check_cu(const gdn_tensor* cu, int64_t n_seq, int64_t t_total, hipStream_t s) {
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
   if (hipStreamIsCapturing(s, &cs) != hipSuccess) return fail(GDN_ERR_HIP, "hipStreamIsCapturing failed");
   if (cs != hipStreamCaptureStatusNone) return GDN_OK;
   int32_t* word = nullptr;
   hipError_t e = gdn::debug_word_region(&word);
   if (e == hipSuccess)
-    e = gdn::launch_check_cu(cu->data, cu->dtype == GDN_DTYPE_I64, P.n_seq, P.T, word, s);
+    e = gdn::launch_check_cu(cu->data, cu->dtype == GDN_DTYPE_I64, n_seq, t_total, word, s);
   int32_t faults = 0;
   if (e == hipSuccess) e = hipMemcpyAsync(&faults, word, sizeof faults, hipMemcpyDeviceToHost, s);
   if (e == hipSuccess) e = hipStreamSynchronize(s);
@@ -580,7 +600,7 @@ int run(const Problem& P, const gdn_tensor* q, const gdn_tensor* k,
 
   hipError_t e;
   if (P.packed && (P.stages & GDN_STAGE_TABLE) && debug_check_enabled()) {
-    const int rc = debug_check_cu(P, cu, s);
+    const int rc = debug_check_cu(cu, P.n_seq, P.T, s);
     if (rc) return rc;
   }
   if (P.packed && (P.stages & GDN_STAGE_TABLE)) {
@@ -750,6 +770,10 @@ int run(const Problem& P, const gdn_tensor* q, const gdn_tensor* k,
 }
 
 }  // namespace
+
+int gdn::api_debug_check_cu(const gdn_tensor* cu, int64_t n_seq, int64_t t_total, hipStream_t s) {
+  return debug_check_enabled() ? debug_check_cu(cu, n_seq, t_total, s) : GDN_OK;
+}
 
 extern "C" {
 

@@ -1,0 +1,439 @@
+// gfx950 (CDNA4) kernels around a recurrent layer's projections: the short
+// causal convolution and the residual root-mean-square norm.  Both move each
+// byte once and are bound by HBM (large calls) or by the launch and one trip
+// to memory (small ones).
+#include <hip/hip_runtime.h>
+
+#include "gdn_device.h"
+#include "gdn_layer.h"
+
+namespace gdn {
+
+// ---------------------------------------------------------------------------
+// The short convolution: y[t, c] = bias[c] + sum_j w[c][j] e[t + j, c] (e: a
+// sequence's W - 1 history rows, then its rows), optionally silu.
+//
+// A thread takes 16 bytes' worth of adjacent channels and walks kConvTile
+// tokens with the last W - 1 rows in registers, so a row is read once per
+// tile plus W - 1 rows of overlap that neighbouring tiles find in L2.  The
+// tiles cut the tokens regardless of sequences and leave out each sequence's
+// first W - 1 tokens: those, and the new history, belong to one thread per
+// (sequence, channels) of the second kind of work item, the only one that
+// reads state_in and writes state_out, which may therefore be one array.
+
+constexpr int kConvThreads = 256;
+constexpr int kConvTile = 16;
+
+template <typename TI, bool VEC>
+struct ConvVec {
+  static constexpr int n = VEC ? 16 / (int)sizeof(TI) : 1;
+};
+
+template <typename TI, bool VEC, int E>
+__device__ __forceinline__ void conv_load(float (&v)[E], const TI* p) {
+  if constexpr (VEC) {
+    const uint4 r = ld16(p);
+    const TI* e = (const TI*)&r;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = to_float(e[i]);
+  } else {
+    v[0] = to_float(*p);
+  }
+}
+
+template <typename TI, bool VEC, int E>
+__device__ __forceinline__ void conv_store(TI* p, const float (&v)[E]) {
+  if constexpr (VEC) {
+    uint4 r;
+    TI* e = (TI*)&r;
+#pragma unroll
+    for (int i = 0; i < E; ++i) e[i] = from_float<TI>(v[i]);
+    st16(p, r);
+  } else {
+    *p = from_float<TI>(v[0]);
+  }
+}
+
+// Entry i of cu_seqlens, clamped into [0, t_total].
+__device__ __forceinline__ int conv_cu(const ShortConvParams& p, int i) {
+  const int64_t e = p.cu_i64 ? ((const int64_t*)p.cu)[i] : ((const int32_t*)p.cu)[i];
+  return (int)min(max(e, (int64_t)0), (int64_t)p.t_total);
+}
+
+template <typename TI, int W, bool VEC>
+__global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParams p, int tiles_per_seq,
+                                                                 int n_tiles) {
+  constexpr int E = ConvVec<TI, VEC>::n;
+  const int nvec = (p.d + E - 1) / E;
+  const int64_t u = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+  const int item = (int)(u / nvec);
+  const int c0 = (int)(u - (int64_t)item * nvec) * E;
+  if (item >= n_tiles + p.n_seq) return;
+  const TI* x = (const TI*)p.x + c0;
+  TI* out = (TI*)p.out + c0;
+
+  float w[W][E], bias[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    bias[e] = p.bias ? p.bias[c0 + e] : 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][e] = p.w[(int64_t)(c0 + e) * W + j];
+  }
+  // rows[j]: the raw row W - 1 - j tokens before the current one
+  float rows[W][E];
+  auto emit = [&](int64_t t) {
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float a = bias[e];
+#pragma unroll
+      for (int j = 0; j < W; ++j) a += w[j][e] * rows[j][e];
+      y[e] = p.silu ? silu_f32(a) : a;
+    }
+    conv_store<TI, VEC>(out + t * p.o_st, y);
+  };
+  auto shift = [&]() {
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+      for (int e = 0; e < E; ++e) rows[j][e] = rows[j + 1][e];
+  };
+
+  if (item < n_tiles) {
+    // tokens [t0, t1), the current sequence's start and end
+    int t0, t1, start, end, seq = 0, last = 0;
+    if (p.cu) {
+      t0 = item * kConvTile;
+      t1 = min(t0 + kConvTile, conv_cu(p, p.n_seq));
+      int lo = 0, hi = p.n_seq - 1;  // largest sequence starting at or before t0
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (conv_cu(p, mid) <= t0) lo = mid; else hi = mid - 1;
+      }
+      seq = lo;
+      last = p.n_seq - 1;
+      start = conv_cu(p, seq);
+      end = conv_cu(p, seq + 1);
+    } else {
+      seq = last = item / tiles_per_seq;
+      start = seq * p.seq_len;
+      end = start + p.seq_len;
+      t0 = start + (item - seq * tiles_per_seq) * kConvTile;
+      t1 = min(t0 + kConvTile, end);
+    }
+    if (t0 >= t1) return;
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j) {
+      const int t = t0 - (W - 1) + j;
+#pragma unroll
+      for (int e = 0; e < E; ++e) rows[j][e] = 0.f;
+      if (t >= 0) conv_load<TI, VEC>(rows[j], x + (int64_t)t * p.x_st);
+    }
+    for (int t = t0; t < t1; ++t) {
+      while (t >= end && seq < last) {
+        ++seq;
+        start = conv_cu(p, seq);
+        end = conv_cu(p, seq + 1);
+      }
+      conv_load<TI, VEC>(rows[W - 1], x + (int64_t)t * p.x_st);
+      if (t - start >= W - 1) emit(t);
+      shift();
+    }
+    return;
+  }
+
+  // A sequence's first W - 1 tokens and its new history.
+  const int seq = item - n_tiles;
+  int start, len;
+  if (p.cu) {
+    start = conv_cu(p, seq);
+    len = max(conv_cu(p, seq + 1) - start, 0);
+  } else {
+    start = seq * p.seq_len;
+    len = p.seq_len;
+  }
+  const TI* hin = p.state_in ? (const TI*)p.state_in + (int64_t)seq * (W - 1) * p.d + c0 : nullptr;
+  float hist[W][E];
+#pragma unroll
+  for (int j = 0; j + 1 < W; ++j) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) rows[j][e] = 0.f;
+    if (hin) conv_load<TI, VEC>(rows[j], hin + (int64_t)j * p.d);
+#pragma unroll
+    for (int e = 0; e < E; ++e) hist[j][e] = rows[j][e];
+  }
+#pragma unroll
+  for (int i = 0; i + 1 < W; ++i) {
+    if (i < len) {
+      conv_load<TI, VEC>(rows[W - 1], x + (int64_t)(start + i) * p.x_st);
+      emit(start + i);
+      shift();
+    }
+  }
+  if (!p.state_out) return;
+  TI* hout = (TI*)p.state_out + (int64_t)seq * (W - 1) * p.d + c0;
+  float tail[W][E];
+#pragma unroll
+  for (int j = 0; j + 1 < W; ++j) {
+    const int r = len + j;  // of the history followed by the sequence
+    if (r >= W - 1) {
+      conv_load<TI, VEC>(tail[j], x + (int64_t)(start + r - (W - 1)) * p.x_st);
+    } else {
+#pragma unroll
+      for (int k = 0; k + 1 < W; ++k)
+        if (k == r)
+#pragma unroll
+          for (int e = 0; e < E; ++e) tail[j][e] = hist[k][e];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j + 1 < W; ++j) conv_store<TI, VEC>(hout + (int64_t)j * p.d, tail[j]);
+}
+
+template <typename TI, bool VEC>
+static hipError_t launch_short_conv_t(const ShortConvParams& p, hipStream_t s) {
+  constexpr int E = ConvVec<TI, VEC>::n;
+  const int64_t nvec = (p.d + E - 1) / E;
+  // sequences of fewer than W tokens have no tokens for the tiles
+  const int64_t per_seq = p.cu ? 0 : p.seq_len < p.width ? 0 : (p.seq_len + kConvTile - 1) / kConvTile;
+  const int64_t tiles = p.cu ? ((int64_t)p.t_total + kConvTile - 1) / kConvTile : per_seq * p.n_seq;
+  const int64_t items = tiles + p.n_seq;
+  const int64_t blocks = (items * nvec + kConvThreads - 1) / kConvThreads;
+  if (items >= ((int64_t)1 << 31) || blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  if (blocks == 0) return hipSuccess;
+  switch (p.width) {
+#define GDN_CONV(W)                                                                                        \
+    case W:                                                                                                \
+      hipLaunchKernelGGL((short_conv_kernel<TI, W, VEC>), dim3((unsigned)blocks), dim3(kConvThreads), 0, s, p, \
+                         (int)per_seq, (int)tiles);                                                        \
+      return hipGetLastError();
+    GDN_CONV(1) GDN_CONV(2) GDN_CONV(3) GDN_CONV(4)
+#undef GDN_CONV
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_short_conv(bool bf16, bool vec, const ShortConvParams& p, hipStream_t s) {
+  if (bf16) return vec ? launch_short_conv_t<gdn::bf16, true>(p, s) : launch_short_conv_t<gdn::bf16, false>(p, s);
+  return vec ? launch_short_conv_t<float, true>(p, s) : launch_short_conv_t<float, false>(p, s);
+}
+
+// ---------------------------------------------------------------------------
+// The residual norm: r = x + residual, y = r / sqrt(mean r^2 + eps) * w, with
+// y in the input's type, in e4m3 with a scale per row or per 128 columns, or
+// both.
+//
+// TPR threads hold a row in registers, each NV vectors of eight adjacent
+// columns, so the row is read once and the two reductions (the sum of
+// squares; the largest |y|, of a row, or of the 16 lanes that hold a group)
+// run on registers.  Rows of up to 1024 columns take one wave each, longer
+// ones a workgroup.
+
+constexpr int kNormVec = 8;
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleFloor = 0x1p-100f;  // keeps a scale and its reciprocal finite
+
+// The larger of two non-negative floats; a NaN (its bits are the larger
+// integer) wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+
+// Eight columns from c0 on, those at or after d as zeros.
+template <typename TI, bool VEC>
+__device__ __forceinline__ void norm_load(float (&v)[kNormVec], const TI* row, int c0, int d) {
+  if constexpr (VEC) {
+    if constexpr (sizeof(TI) == 2) {
+      const uint4 r = ld16(row + c0);
+      const TI* e = (const TI*)&r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
+    } else {
+      const f32x4 a = *(const f32x4*)(row + c0), b = *(const f32x4*)(row + c0 + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c0 + i < d ? to_float(row[c0 + i]) : 0.f;
+  }
+}
+
+template <typename TI, bool VEC>
+__device__ __forceinline__ void norm_store(TI* row, const float (&v)[kNormVec], int c0, int d) {
+  if constexpr (VEC) {
+    if constexpr (sizeof(TI) == 2) {
+      uint4 r;
+      TI* e = (TI*)&r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = from_float<TI>(v[i]);
+      st16(row + c0, r);
+    } else {
+      f32x4 a, b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = v[i];
+        b[i] = v[4 + i];
+      }
+      *(f32x4*)(row + c0) = a;
+      *(f32x4*)(row + c0 + 4) = b;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < d) row[c0 + i] = from_float<TI>(v[i]);
+  }
+}
+
+// Eight columns times inv as e4m3 (the hardware conversion rounds to nearest
+// even; |v inv| is at most 448 up to fp32 rounding, and everything below 464
+// rounds into the range).
+template <bool VEC>
+__device__ __forceinline__ void norm_store_q(uint8_t* row, const float (&v)[kNormVec], float inv, int c0,
+                                             int d) {
+  int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, a, true);
+  int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
+  b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, b, true);
+  if constexpr (VEC) {
+    *(uint2*)(row + c0) = make_uint2((unsigned)a, (unsigned)b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < d) row[c0 + i] = (uint8_t)((i < 4 ? a : b) >> (8 * (i & 3)));
+  }
+}
+
+// A reduction over the TPR threads of a row (one wave, or the workgroup).
+template <int TPR, typename F>
+__device__ __forceinline__ float row_reduce(float v, float* lds, F f) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = f(v, __shfl_xor(v, off));
+  if constexpr (TPR > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) lds[wave] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 64; ++i) v = f(v, lds[i]);
+  }
+  return v;
+}
+
+template <typename TI, int TPR, int NV, bool VEC>
+__global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(NormParams p) {
+  constexpr int RPB = TPR > 64 ? 1 : 4;  // rows per workgroup
+  __shared__ float s_sum[16], s_max[16];
+  const int sub = TPR > 64 ? threadIdx.x : threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * RPB + (TPR > 64 ? 0 : threadIdx.x >> 6);
+  if (row >= p.rows) return;
+  const TI* x = (const TI*)p.x + row * p.x_st;
+  const TI* res = p.res ? (const TI*)p.res + row * p.r_st : nullptr;
+  float v[NV][kNormVec];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c0 = (sub + i * TPR) * kNormVec;
+#pragma unroll
+    for (int e = 0; e < kNormVec; ++e) v[i][e] = 0.f;
+    if (c0 < p.d) {
+      norm_load<TI, VEC>(v[i], x, c0, p.d);
+      if (res) {
+        float r[kNormVec];
+        norm_load<TI, VEC>(r, res, c0, p.d);
+#pragma unroll
+        for (int e = 0; e < kNormVec; ++e) v[i][e] += r[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c0 = (sub + i * TPR) * kNormVec;
+    if (p.res_out && c0 < p.d) norm_store<TI, VEC>((TI*)p.res_out + row * p.ro_st, v[i], c0, p.d);
+#pragma unroll
+    for (int e = 0; e < kNormVec; ++e) ss += v[i][e] * v[i][e];
+  }
+  ss = row_reduce<TPR>(ss, s_sum, [](float a, float b) { return a + b; });
+  const float rn = 1.f / sqrtf(ss / (float)p.d + p.eps);
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c0 = (sub + i * TPR) * kNormVec;
+    const bool live = c0 < p.d;
+    float top = 0.f;
+    if (live) {
+      float w[kNormVec];
+      if (p.w) {
+        norm_load<float, VEC>(w, p.w, c0, p.d);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kNormVec; ++e) w[e] = 1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kNormVec; ++e) {
+        v[i][e] = v[i][e] * rn * w[e];
+        if (VEC || c0 + e < p.d) top = max_nan(top, fabsf(v[i][e]));
+      }
+      if (p.out) norm_store<TI, VEC>((TI*)p.out + row * p.o_st, v[i], c0, p.d);
+    }
+    if (p.out_q && p.groups) {
+      // a group's 128 columns are 16 adjacent lanes, all of them here (those
+      // past the row's end with a maximum of zero)
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) top = max_nan(top, __shfl_xor(top, off));
+      const float scale = max_nan(top, kScaleFloor) / kE4m3Max;
+      if (live) {
+        norm_store_q<VEC>(p.out_q + row * p.q_st, v[i], 1.f / scale, c0, p.d);
+        if ((sub & 15) == 0) p.scales[row * p.groups + c0 / 128] = scale;
+      }
+    }
+    big = max_nan(big, top);
+  }
+  if (p.out_q && !p.groups) {
+    big = row_reduce<TPR>(big, s_max, [](float a, float b) { return max_nan(a, b); });
+    const float scale = max_nan(big, kScaleFloor) / kE4m3Max;
+    const float inv = 1.f / scale;
+    if (sub == 0) p.scales[row] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c0 = (sub + i * TPR) * kNormVec;
+      if (c0 < p.d) norm_store_q<VEC>(p.out_q + row * p.q_st, v[i], inv, c0, p.d);
+    }
+  }
+}
+
+template <typename TI, bool VEC>
+static hipError_t launch_add_rms_norm_t(const NormParams& p, hipStream_t s) {
+  const int vecs = (p.d + kNormVec - 1) / kNormVec;
+  const bool wave = vecs <= 128;
+  const int64_t blocks = wave ? (p.rows + 3) / 4 : p.rows;
+  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+#define GDN_NORM(TPR, NV)                                                                             \
+  do {                                                                                                \
+    hipLaunchKernelGGL((add_rms_norm_kernel<TI, TPR, NV, VEC>), dim3((unsigned)blocks),                \
+                       dim3(TPR > 64 ? TPR : 256), 0, s, p);                                          \
+    return hipGetLastError();                                                                         \
+  } while (0)
+  if (vecs <= 64) GDN_NORM(64, 1);
+  if (vecs <= 128) GDN_NORM(64, 2);
+  if (vecs <= 256) GDN_NORM(256, 1);
+  if (vecs <= 512) GDN_NORM(256, 2);
+  if (vecs <= 768) GDN_NORM(256, 3);
+  if (vecs <= 1024) GDN_NORM(256, 4);
+  if (vecs <= 2048) GDN_NORM(1024, 2);
+  if (vecs <= 4096) GDN_NORM(1024, 4);
+  if (vecs <= 8192) GDN_NORM(1024, 8);
+#undef GDN_NORM
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& p, hipStream_t s) {
+  if (p.rows <= 0) return hipSuccess;
+  if (bf16) return vec ? launch_add_rms_norm_t<gdn::bf16, true>(p, s) : launch_add_rms_norm_t<gdn::bf16, false>(p, s);
+  return vec ? launch_add_rms_norm_t<float, true>(p, s) : launch_add_rms_norm_t<float, false>(p, s);
+}
+
+}  // namespace gdn

@@ -61,7 +61,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 9
+#define GDN_ABI_VERSION 10
 
 /* Status codes. */
 #define GDN_OK 0
@@ -79,6 +79,9 @@ extern "C" {
 #define GDN_DTYPE_F32 2
 #define GDN_DTYPE_I32 3
 #define GDN_DTYPE_I64 4
+/* 8-bit float, 4 exponent and 3 mantissa bits, no infinities, largest value
+ * 448: an output type of gdn_add_rms_norm only.                            */
+#define GDN_E4M3 5
 
 /* A strided view of caller-owned memory (device memory for every tensor
  * argument).  shape/stride have ndim valid entries, outermost first; strides
@@ -468,6 +471,143 @@ int gdn_output_gate(const gdn_tensor* x, const gdn_tensor* z, const float* weigh
  * GDN_ERR_NULL_ARG / GDN_ERR_SHAPE for a NULL table or n_seq < 1.
  */
 int gdn_check_cu_seqlens(const int32_t* cu_host, int64_t n_seq, int64_t t_total);
+
+/* ------------------------------------------------------------------------
+ * The operators around a recurrent layer's projections.  They share the
+ * conventions above: tensors as descriptors, packed batches by cu_seqlens
+ * (int32 or int64, clamped on the device, checked with GDN_DEBUG_CHECK=1),
+ * validation on the host before any HIP call, work enqueued on the caller's
+ * stream, nothing allocated, no synchronisation.  An output may share memory
+ * with an input only where its description says so; other overlaps are
+ * GDN_ERR_LAYOUT.  All sums, norms and states are fp32, and each output is
+ * rounded once.
+ */
+
+/*
+ * gdn_short_conv -- the causal depthwise convolution along the tokens of
+ * each sequence that a recurrent layer runs on its projections (the one
+ * GDN_FLAG_QKV_CONV fuses into the delta-rule prefill), on its own and over
+ * any channels:
+ *     y[t, c] = bias[c] + sum_{j=0}^{W-1} weight[c][j] * e[t + j, c],
+ * e being the sequence's W - 1 history rows (state_in, or zeros) followed by
+ * its rows; then silu(y) = y / (1 + e^-y) with GDN_CONV_SILU.
+ *   x, out     [T, D] (one sequence, or packed by cu_seqlens) or [B, L, D]
+ *              (B sequences of L tokens; L = 1 is one step for each of B
+ *              running sequences); bf16 or f32; unit stride in the last
+ *              dimension, token stride any; [B, L, D] with stride[0] ==
+ *              L * stride[1].  16-byte vector accesses are used where D,
+ *              the strides and the addresses allow, else element accesses.
+ *   weight     f32 [D][W] contiguous device array, W = 1 .. 4, the last tap
+ *              on the current token; bias f32 [D] or NULL
+ *   cu_seqlens [N + 1] device array or NULL, as gdn_prefill; rows at or
+ *              after cu[N] are not written
+ *   state_in   [N, W - 1, D] of x's dtype, contiguous, or NULL for zeros
+ *   state_out  the last W - 1 rows of e for each sequence, the same layout,
+ *              or NULL (not written); it may be state_in
+ * Returns a GDN_* status; validation errors enqueue nothing.
+ */
+#define GDN_CONV_SILU 1u
+int gdn_short_conv(const gdn_tensor* x, const gdn_tensor* weight, const float* bias,
+                   const gdn_tensor* cu_seqlens, const gdn_tensor* state_in,
+                   gdn_tensor* state_out, gdn_tensor* out, uint32_t flags, void* stream);
+
+/*
+ * The selective state space scan.  For every sequence i and head h (reading
+ * group h / (H/G) of b and c), from the N x P state S = init_state[i, h] (or
+ * zeros):
+ *     d_t = softplus(dt[t, h] + dt_bias[h])      (GDN_SSM_SOFTPLUS; else
+ *                                                 d_t = dt[t, h] + dt_bias[h])
+ *     S   = exp(-exp(a_log[h]) d_t) S + d_t b_t x_t^T
+ *     out[t, h] = S^T c_t + d_skip[h] x_t
+ * and final_state[i, h] = S after the last token.  The state is laid out as
+ * the delta rule's (d_k x d_v, here N x P), so both mixers' states can share
+ * one pool.  d_t >= 0 is a precondition without GDN_SSM_SOFTPLUS.  Inputs
+ * are expected to be finite: a NaN or infinity reaches the later tokens of
+ * its own sequence and may reach up to 63 earlier ones; it never reaches
+ * another sequence or head.
+ */
+#define GDN_SSM_SOFTPLUS 1u
+typedef struct gdn_ssm_options {
+  const float* a_log;    /* f32 [H] device array, or NULL for zeros (rate 1)  */
+  const float* dt_bias;  /* f32 [H] device array, or NULL for zeros           */
+  const float* d_skip;   /* f32 [H] device array, or NULL (no skip)           */
+  uint32_t flags;        /* GDN_SSM_* (default GDN_SSM_SOFTPLUS)              */
+  /* Segments: a sequence's transition is one number per token and head, so
+   * it can be cut into segments whose end states are formed at once (each
+   * from zero), joined in order, and then scanned at once.  0 (default):
+   * automatic; -1: one pass over each sequence; n > 0: segments of n blocks
+   * of 64 tokens (the results differ in rounding).                          */
+  int32_t segment_blocks;
+} gdn_ssm_options;
+
+/* Fills *opts with the defaults listed in gdn_ssm_options. */
+void gdn_ssm_default_options(gdn_ssm_options* opts);
+
+/*
+ * gdn_ssm_prefill -- the scan over prompts.
+ *   x, out      [T, H, P] or [B, T/B, H, P]; bf16 or f32
+ *   dt          [T, H] (or [B, T/B, H]) f32
+ *   b, c        [T, G, N] (or 4-D); x's dtype; H a multiple of G
+ *   cu_seqlens, init_state, final_state ([Nseq, H, N, P] f32)  as
+ *               gdn_prefill; final_state may be init_state
+ *   opts        NULL for the defaults
+ *   workspace   gdn_ssm_workspace_size() bytes of device memory, 256-byte
+ *               aligned (NULL if that is 0); not to be used by another call
+ *               that overlaps on the device
+ * Sizes: N, P in {16, 32, 64, 128}; T < 2^31; layout of x, b, c and out as
+ * gdn_prefill's (16-byte vector accesses, else GDN_ERR_LAYOUT).
+ */
+int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor* b,
+                    const gdn_tensor* c, const gdn_tensor* cu_seqlens,
+                    const gdn_tensor* init_state, gdn_tensor* out, gdn_tensor* final_state,
+                    const gdn_ssm_options* opts, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Workspace bytes of gdn_ssm_prefill for these shapes (host only; the data
+ * pointers are not read). */
+int gdn_ssm_workspace_size(const gdn_tensor* x, const gdn_tensor* b,
+                           const gdn_tensor* cu_seqlens, const gdn_ssm_options* opts,
+                           size_t* bytes);
+
+/*
+ * gdn_ssm_decode -- the scan of one token for each of Nseq running
+ * sequences, on their states in place.
+ *   x, out  [Nseq, H, P]; dt [Nseq, H] f32; b, c [Nseq, G, N]; one dtype,
+ *           bf16 or f32, for x, b, c and out
+ *   state   f32 [Nseq, H, N, P] contiguous, 16-byte aligned, read and written
+ *   opts    NULL for the defaults (segment_blocks is ignored)
+ * x and out rows start on 4-element boundaries (address and strides); N, P
+ * in {16, 32, 64, 128}.  Nseq = 0 enqueues nothing.
+ */
+int gdn_ssm_decode(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor* b,
+                   const gdn_tensor* c, gdn_tensor* state, gdn_tensor* out,
+                   const gdn_ssm_options* opts, void* stream);
+
+/*
+ * gdn_add_rms_norm -- the residual's addition and the root-mean-square norm
+ * before a layer's projections, with its output in the input's type, in 8
+ * bits with scales, or both:
+ *     r = x + residual (residual NULL: r = x),  residual_out = r,
+ *     y = r / sqrt(mean(r^2) + eps) * weight,   out = y,
+ *     scales = max(max|y|, 2^-100) / 448,       out_q = y / scales
+ * over rows of D elements.  r is kept in fp32 for the norm (residual_out is
+ * its rounding); the maximum is taken over each row, or over each 128
+ * columns (the last group may be shorter).  out_q rounds to nearest even;
+ * dequantised values are out_q * scales.  A NaN anywhere in a row makes the
+ * row's y and scales NaN.
+ *   x, residual, residual_out, out  [R, D]; one dtype, bf16 or f32
+ *   out_q   [R, D] GDN_E4M3;  scales  f32 contiguous, [R] (rows) or
+ *           [R, ceil(D / 128)] (groups); both or neither
+ *   weight  f32 [D] device array, or NULL for ones;  eps >= 0
+ * residual, residual_out, out, out_q with scales, each may be NULL, but not
+ * all outputs.  Unit stride in the last dimension, row stride any; 16-byte
+ * accesses are used where D, strides and addresses allow.  residual_out may
+ * be x or residual, and out may be x or residual (same memory and strides).
+ * D <= 65536.
+ */
+int gdn_add_rms_norm(const gdn_tensor* x, const gdn_tensor* residual, const float* weight,
+                     float eps, gdn_tensor* residual_out, gdn_tensor* out, gdn_tensor* out_q,
+                     gdn_tensor* scales, void* stream);
 
 /* Short description of a status code (static storage). */
 const char* gdn_status_string(int status);
