@@ -38,6 +38,7 @@ struct SsmParams {
   const float* d_skip;
   int64_t x_st, x_sh, dt_st, dt_sh, b_st, b_sh, c_st, c_sh, o_st, o_sh;
   int32_t heads, group;  // heads, heads per group
+  int32_t unit;          // heads per XCD unit (set by the launcher)
   int32_t softplus;
   // segments: n_seq sequences; uniform ones have seq_len tokens and
   // segs_per_seq segments of seg_len tokens (the last may be shorter), packed

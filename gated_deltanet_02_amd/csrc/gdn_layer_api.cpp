@@ -168,6 +168,25 @@ bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
 bool head_dim(int64_t d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
+// A token stride the scan's 32-bit offsets inside a block can use; a single
+// token's stride is never taken, and replaced by the row's own length.
+constexpr int64_t kMaxTokenStride = (int64_t)1 << 24;
+
+int token_stride(const char* name, int64_t row, Tokens* v) {
+  if (v->T <= 1) v->st = row;
+  if (v->st > kMaxTokenStride)
+    return api_fail(GDN_ERR_LAYOUT, "%s: token stride must be at most 2^24 elements", name);
+  return GDN_OK;
+}
+
+// Rows [tokens][heads][row] of an output that overlap each other would race.
+int check_rows(const char* name, int64_t tokens, int64_t st, int64_t heads, int64_t sh, int64_t row) {
+  const bool token_major = (heads <= 1 || sh >= row) && (tokens <= 1 || st >= (heads - 1) * sh + row);
+  const bool head_major = (tokens <= 1 || st >= row) && (heads <= 1 || sh >= (tokens - 1) * st + row);
+  if (tokens > 0 && !token_major && !head_major) return api_fail(GDN_ERR_LAYOUT, "%s: rows overlap", name);
+  return GDN_OK;
+}
+
 // The scan's sizes, layout and segments.
 struct Ssm {
   bool bf16 = true;
@@ -195,9 +214,11 @@ int ssm_options(const gdn_ssm_options* opts, gdn_ssm_options* o) {
 constexpr int64_t kMaxSegment = (int64_t)1 << 20;
 constexpr int64_t kMinAutoBlocks = 4;
 
-// Tokens per segment.  The automatic choice spreads all tokens x heads over
-// the workgroups that fill the chip, so that a few long sequences do not
-// leave it idle, in segments of at least four blocks.
+// Tokens per segment.  The automatic choice spreads the tokens x heads over
+// the workgroups that run at once, so that a few long sequences do not leave
+// the chip idle, in segments of at least four blocks: of uniform sequences,
+// as many equal segments as fit those workgroups in one round; of packed
+// ones, whose lengths the host does not know, an equal share of all blocks.
 int64_t ssm_segment_tokens(const Ssm& P) {
   const int64_t block = gdn::kSsmBlock;
   int64_t blocks;
@@ -206,9 +227,15 @@ int64_t ssm_segment_tokens(const Ssm& P) {
   } else if (P.opts.segment_blocks < 0) {
     blocks = kMaxSegment / block;
   } else {
-    const int64_t all = ((P.T + block - 1) / block) * P.H;
     const int64_t target = gdn::ssm_target_groups();
-    blocks = std::max(kMinAutoBlocks, (all + target - 1) / target);
+    if (P.seq.packed) {
+      blocks = (((P.T + block - 1) / block) * P.H + target - 1) / target;
+    } else {
+      const int64_t all = (P.seq.len + block - 1) / block;
+      const int64_t segs = std::max<int64_t>(1, target / (P.H * P.seq.n));
+      blocks = (all + segs - 1) / segs;
+    }
+    blocks = std::max(kMinAutoBlocks, blocks);
   }
   return std::min(blocks * block, kMaxSegment);
 }
@@ -336,6 +363,7 @@ int gdn_short_conv(const gdn_tensor* x, const gdn_tensor* weight, const float* b
                       (long long)D);
     if (!is_empty(t) && !contiguous(t)) return api_fail(GDN_ERR_LAYOUT, "%s must be contiguous", names[i]);
   }
+  if ((rc = check_rows("out", tx.T, to.st, 1, 0, D))) return rc;
   const Range outs[2] = {range_of(out, "out"), range_of(state_out, "state_out")};
   const Range ins[5] = {range_of(x, "x"), range_of(weight, "weight"), range_of(bias, 4 * D, "bias"),
                         range_of(cu_seqlens, "cu_seqlens"),
@@ -427,6 +455,10 @@ int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor*
         return api_fail(GDN_ERR_LAYOUT, "%s: token/head strides must be multiples of %lld elements", v.n,
                         (long long)epg);
     }
+  if ((rc = check_rows("out", P.T, P.o.st, P.H, out->stride[r - 2], P.P)) || (rc = token_stride("x", P.P, &P.x)) ||
+      (rc = token_stride("b", P.N, &P.b)) || (rc = token_stride("c", P.N, &P.c)) ||
+      (rc = token_stride("out", P.P, &P.o)))
+    return rc;
   if (init_state && (rc = check_state(init_state, "init_state", P.seq.n, P))) return rc;
   if (final_state && (rc = check_state(final_state, "final_state", P.seq.n, P))) return rc;
   if (P.total > 0 && (!workspace || workspace_bytes < P.total))
@@ -536,6 +568,7 @@ int gdn_ssm_decode(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor* 
   for (const auto& v : rows)
     if ((uintptr_t)v.t->data % (uintptr_t)(4 * es) || v.t->stride[0] % 4 || v.t->stride[1] % 4)
       return api_fail(GDN_ERR_LAYOUT, "%s rows must start on 4-element boundaries", v.name);
+  if ((rc = check_rows("out", n, out->stride[0], P.H, out->stride[1], P.P))) return rc;
   const Range outs[2] = {range_of(out, "out"), range_of(state, "state")};
   const Range ins[7] = {range_of(x, "x"), range_of(dt, "dt"), range_of(b, "b"), range_of(c, "c"),
                         range_of(P.opts.a_log, 4 * P.H, "a_log"), range_of(P.opts.dt_bias, 4 * P.H, "dt_bias"),
@@ -615,9 +648,7 @@ int gdn_add_rms_norm(const gdn_tensor* x, const gdn_tensor* residual, const floa
         return api_fail(GDN_ERR_LAYOUT, "%s overlaps %s", outs[i].name, ins[j].name);
     for (int j = i + 1; j < 4; ++j)
       if (overlap(outs[i], outs[j])) return api_fail(GDN_ERR_LAYOUT, "%s overlaps %s", outs[i].name, outs[j].name);
-    // rows of an output that overlap each other would race
-    if (out_ts[i] && out_ts[i]->ndim == 2 && R > 1 && out_ts[i]->stride[0] < D && i < 3)
-      return api_fail(GDN_ERR_LAYOUT, "%s: rows overlap", outs[i].name);
+    if (i < 3 && out_ts[i] && (rc = check_rows(outs[i].name, R, out_ts[i]->stride[0], 1, 0, D))) return rc;
   }
   const int64_t epg = x->dtype == GDN_DTYPE_BF16 ? 8 : 4;
   bool vec = D % 8 == 0 && aligned16(weight);

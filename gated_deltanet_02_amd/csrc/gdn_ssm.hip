@@ -30,6 +30,8 @@
 // order, and the scan of all segments at once.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "gdn_device.h"
 #include "gdn_layer.h"
 
@@ -37,31 +39,27 @@ namespace gdn {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <typename TI, int N, int P>
+// HP: heads (of one group) that a workgroup takes.
+template <typename TI, int N, int P, int HP, bool OUT>
 struct SsmShape {
   static constexpr int S = sizeof(TI);
-  static constexpr int GE = 16 / S;                 // elements per 16-byte granule
-  static constexpr int C = S == 2 ? 64 : 32;        // tokens per block
-  static constexpr int NW = P >= 64 ? 4 : P / 16;   // waves
+  static constexpr int C = 32;                      // tokens per block
+  static constexpr int CW = 16;                     // state columns per wave
+  static constexpr int NH = P / CW, NW = NH * HP;   // waves of a head, of all
   static constexpr int THREADS = 64 * NW;
-  static constexpr int CW = P / NW;                 // state columns per wave
   static constexpr int CT = CW / 16, RT = C / 16, NT = N / 16;
   static constexpr int TPU = S == 2 ? 2 : 1;        // 16-wide tiles per unit
   static constexpr int NU = (NT + TPU - 1) / TPU;   // units along N
   static constexpr bool HALF = TPU == 2 && NT % 2 == 1;  // N = 16: half a unit
   static constexpr int TU = RT / TPU;               // units along the tokens
-  static constexpr int GRB = N / GE, GRX = P / GE;  // granules per row of b (c) and x
-  static constexpr int MU = S == 2 ? 6 : 3;         // units of M (row tile it: it / TPU + 1)
-  static constexpr int o_b = 0, o_c = C * N * S, o_x = 2 * C * N * S, o_m = o_x + C * P * S;
-  static constexpr int o_ml = o_m + MU * 1024;      // M's second terms
-  static constexpr int o_w = o_ml + (S == 2 ? MU * 1024 : 0);
-  static constexpr int total = o_w + 5 * C * 4;     // cum (two terms), d, w, e
-  // first unit of row tile it of M
-  static constexpr int mu0(int it) {
-    int u = 0;
-    for (int i = 0; i < it; ++i) u += i / TPU + 1;
-    return u;
-  }
+  static constexpr int TILES = RT * (RT + 1) / 2;   // of M
+  // LDS: rings of b (and c), of x, of the blocks' decays, and M's two buffers
+  static constexpr int BB = C * N * S, XB = C * P * S, MB = 3072, WB = 4 * C * 4;
+  static constexpr int RB = OUT ? 3 : 4, RX = OUT ? 2 : 4, RW = 4;
+  static constexpr int bc = BB * (OUT ? 2 : 1);     // b, then c
+  // (each head has its own x, M and decays)
+  static constexpr int o_x = RB * bc, o_m = o_x + HP * RX * XB, o_w = o_m + (OUT ? HP * 2 * MB : 0);
+  static constexpr int total = o_w + HP * RW * WB;
 };
 
 // Granule g of a row sits at granule g ^ swizzle: the four rows of a lane
@@ -80,25 +78,54 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// A unit of row `row` of b or c (elements of the 16-wide k-tiles 2u, 2u + 1).
-template <typename TI, int GR, bool HALF>
-__device__ __forceinline__ typename Unit<TI>::type ssm_row_unit(const char* tile, int row, int u, int q) {
-  if constexpr (HALF) {
-    const uint2 r = *(const uint2*)(tile + row * GR * 16 + (((q >> 1) ^ ssm_swz<GR>(row)) * 16) + (q & 1) * 8);
-    return __builtin_bit_cast(bf16x8, make_uint4(r.x, r.y, 0u, 0u));
-  } else {
-    return *(const typename Unit<TI>::type*)(tile + row * GR * 16 + (((4 * u + q) ^ ssm_swz<GR>(row)) * 16));
-  }
+// The same without a wait: for the copying wave, which waits for its copies
+// itself, and its partner before the first block.
+__device__ __forceinline__ void ssm_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
-// Byte offset in a row of b or c of the four elements 16 nt + 4 k .. + 3.
+// First row of lane group q's four rows of state tile nt.  bf16 pairs the
+// tiles (2u, 2u + 1) so that a lane's rows of the pair are eight consecutive
+// ones, the granule of a row of b or c that it meets.
 template <typename TI, int N>
-__device__ __forceinline__ int ssm_quad(int row, int nt, int k) {
-  constexpr int GR = N * (int)sizeof(TI) / 16;
-  if constexpr (sizeof(TI) == 4) return ((4 * nt + k) ^ ssm_swz<GR>(row)) * 16;
-  else if constexpr (N == 16) return ((k >> 1) ^ ssm_swz<GR>(row)) * 16 + (k & 1) * 8;
-  else return ((4 * (nt >> 1) + k) ^ ssm_swz<GR>(row)) * 16 + (nt & 1) * 8;
+__device__ __forceinline__ int ssm_state_row(int nt, int q) {
+  if (sizeof(TI) == 2 && N >= 32) return 32 * (nt >> 1) + 8 * q + 4 * (nt & 1);
+  return 16 * nt + 4 * q;
 }
+
+// Operand reads from the tiles.  Everything but the lane's own place is a
+// compile-time constant: rows 16 apart have the same swizzle, and unit u of a
+// row differs from unit 0 by an exclusive or in the granule's upper bits.
+template <typename TI, int N>
+struct SsmRows {
+  static constexpr int RB = N * (int)sizeof(TI), GR = RB / 16;
+  static constexpr bool HALF = RB == 32;  // bf16, N = 16: half a unit
+  uint32_t row;  // of unit 0 of row l % 16
+  uint32_t col;  // of the transposed read's first quad, column tile 0
+  __device__ __forceinline__ SsmRows(int lane) {
+    const int q = lane >> 4, m = lane & 15, k = lane & 3, r = 4 * q + ((lane >> 2) & 3);
+    if constexpr (HALF) {
+      row = m * RB + (((q >> 1) ^ ssm_swz<GR>(m)) * 16) + (q & 1) * 8;
+      col = r * RB + (((k >> 1) ^ ssm_swz<GR>(r)) * 16) + (k & 1) * 8;
+    } else {
+      row = m * RB + ((q ^ ssm_swz<GR>(m)) * 16);
+      col = r * RB + ((k ^ ssm_swz<GR>(r)) * 16);
+    }
+  }
+  // unit u of row 16 it + l % 16 (`it` may be a run-time value)
+  __device__ __forceinline__ typename Unit<TI>::type unit(const char* tile, int it, int u) const {
+    if constexpr (HALF) {
+      const uint2 r = *(const uint2*)(tile + row + it * 16 * RB);
+      return __builtin_bit_cast(bf16x8, make_uint4(r.x, r.y, 0u, 0u));
+    } else {
+      return *(const typename Unit<TI>::type*)(tile + (row ^ (u * 64)) + it * 16 * RB);
+    }
+  }
+  // column 16 nt + l % 16 over the tokens of unit tu
+  __device__ __forceinline__ typename Unit<TI>::type column(const char* tile, int nt, int tu, int lane) const;
+};
 
 // The LDS transpose read: lane j of a 16-lane group gets element j % 4 of
 // the 8 bytes that lane 4 k + j / 4 names, as its element k.
@@ -110,102 +137,154 @@ __device__ __forceinline__ bf16x8 ssm_tr(const char* lo, const char* hi) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Column 16 nt + l % 16 of b over the tokens of unit tu (b read transposed).
 template <typename TI, int N>
-__device__ __forceinline__ typename Unit<TI>::type ssm_b_col(const char* tile, int nt, int tu, int lane) {
-  constexpr int RB = N * (int)sizeof(TI);
-  const int q = lane >> 4, j = lane & 15;
+__device__ __forceinline__ typename Unit<TI>::type SsmRows<TI, N>::column(const char* tile, int nt, int tu,
+                                                                         int lane) const {
   if constexpr (sizeof(TI) == 2) {
-    const int r = 32 * tu + 4 * q + (j >> 2);
-    return ssm_tr(tile + r * RB + ssm_quad<TI, N>(r, nt, j & 3),
-                  tile + (r + 16) * RB + ssm_quad<TI, N>(r + 16, nt, j & 3));
+    const char* a = tile + (col ^ ((nt >> 1) * 64)) + (nt & 1) * 8 + tu * 32 * RB;
+    return ssm_tr(a, a + 16 * RB);
   } else {
+    const int q = lane >> 4, j = lane & 15;
     f32x4 v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int r = 16 * tu + 4 * q + e;
-      v[e] = *(const float*)(tile + r * RB + ssm_quad<TI, N>(r, nt, j >> 2) + (j & 3) * 4);
+      const int r = 4 * q + e;
+      v[e] = *(const float*)(tile + ((r * RB + (((j >> 2) ^ ssm_swz<GR>(r)) * 16) + (j & 3) * 4) ^ (nt * 64)) +
+                             tu * 16 * RB);
     }
     return v;
   }
 }
 
-// Column col0 + l % 16 of x over the tokens of unit tu.
+// Columns of x (rows in their own order).
 template <typename TI, int P>
-__device__ __forceinline__ typename Unit<TI>::type ssm_x_col(const char* tile, int col0, int tu, int lane) {
-  constexpr int GR = P * (int)sizeof(TI) / 16, RB = P * (int)sizeof(TI);
-  const int q = lane >> 4, j = lane & 15;
-  if constexpr (sizeof(TI) == 2) {
-    const int c = col0 + 4 * (j & 3), g = c >> 3, o = (c & 4) * 2;
-    const int r = 32 * tu + 4 * q + (j >> 2);
-    return ssm_tr(tile + r * RB + ((g ^ ssm_swz<GR>(r)) * 16) + o,
-                  tile + (r + 16) * RB + ((g ^ ssm_swz<GR>(r + 16)) * 16) + o);
-  } else {
-    const int c = col0 + j;
-    f32x4 v;
+struct SsmCols {
+  static constexpr int RB = P * (int)sizeof(TI), GR = RB / 16;
+  uint32_t at[4];  // bf16: [0]; f32: one for each of four rows
+  __device__ __forceinline__ SsmCols(int col0, int lane) {
+    const int q = lane >> 4, j = lane & 15;
+    if constexpr (sizeof(TI) == 2) {
+      const int c = col0 + 4 * (j & 3), r = 4 * q + (j >> 2);
+      at[0] = r * RB + (((c >> 3) ^ ssm_swz<GR>(r)) * 16) + (c & 4) * 2;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = 16 * tu + 4 * q + e;
-      v[e] = *(const float*)(tile + r * RB + (((c >> 2) ^ ssm_swz<GR>(r)) * 16) + (c & 3) * 4);
+      for (int e = 0; e < 4; ++e) {
+        const int c = col0 + j, r = 4 * q + e;
+        at[e] = r * RB + (((c >> 2) ^ ssm_swz<GR>(r)) * 16) + (c & 3) * 4;
+      }
     }
-    return v;
+  }
+  // column col0 + 16 ct + l % 16 over the tokens of unit tu (col0 a multiple
+  // of the wave's columns, so that a column tile is an exclusive or)
+  __device__ __forceinline__ typename Unit<TI>::type column(const char* tile, int ct, int tu) const {
+    if constexpr (sizeof(TI) == 2) {
+      const char* a = tile + (at[0] ^ (ct * 32)) + tu * 32 * RB;
+      return ssm_tr(a, a + 16 * RB);
+    } else {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *(const float*)(tile + (at[e] ^ (ct * 64)) + tu * 16 * RB);
+      return v;
+    }
+  }
+};
+
+// Two floats as TERMS packed bf16 pairs (the first in the low half), each
+// the rounding of what the ones before leave; a term leaves at most 2^-8 of
+// what it rounds, exactly representable as a float.
+template <int TERMS>
+__device__ __forceinline__ void ssm_terms(float a, float b, uint32_t (&t)[TERMS]) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < TERMS; ++i) {
+    bf16x2 v;
+    v[0] = (bf16)a;
+    v[1] = (bf16)b;
+    t[i] = __builtin_bit_cast(uint32_t, v);
+    if (i + 1 < TERMS) {
+      a -= __uint_as_float(t[i] << 16);
+      b -= __uint_as_float(t[i] & 0xffff0000u);
+    }
   }
 }
 
-// x as two bf16 terms (hi + lo within 2^-17 of it), or as it is.
+// Two accumulator tiles' registers as an operand unit in two terms.
 template <bool HALF>
 __device__ __forceinline__ void ssm_split2(const f32x4& t0, const f32x4& t1, bf16x8& hi, bf16x8& lo) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    hi[e] = (bf16)t0[e];
-    lo[e] = (bf16)(t0[e] - (float)hi[e]);
-    hi[4 + e] = HALF ? (bf16)0.f : (bf16)t1[e];
-    lo[4 + e] = HALF ? (bf16)0.f : (bf16)(t1[e] - (float)hi[4 + e]);
+  uint32_t p[4][2];
+  ssm_terms<2>(t0[0], t0[1], p[0]);
+  ssm_terms<2>(t0[2], t0[3], p[1]);
+  if constexpr (!HALF) {
+    ssm_terms<2>(t1[0], t1[1], p[2]);
+    ssm_terms<2>(t1[2], t1[3], p[3]);
+  } else {
+    p[2][0] = p[2][1] = p[3][0] = p[3][1] = 0u;
   }
+  hi = __builtin_bit_cast(bf16x8, make_uint4(p[0][0], p[1][0], p[2][0], p[3][0]));
+  lo = __builtin_bit_cast(bf16x8, make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]));
 }
 
-__device__ __forceinline__ float ssm_step_size(const float* dt_bias, int h, float dt, int softplus) {
-  const float x = dt + (dt_bias ? dt_bias[h] : 0.f);
+__device__ __forceinline__ float ssm_step_size(float bias, float dt, int softplus) {
+  const float x = dt + bias;
   if (!softplus) return x;
   return x > 20.f ? x : log1pf(expf(x));
 }
 
-// Registers of one block's loads: ROWS rows of GR granules by THREADS threads.
-template <int ROWS, int GR, int THREADS>
-struct SsmLoad {
-  static constexpr int rpi = THREADS / GR;  // rows per pass of the workgroup
-  static constexpr int n = (ROWS + rpi - 1) / rpi;
-  static_assert(THREADS % GR == 0, "a pass covers whole rows");
-  uint4 v[n];
-  // rows at or after `rows` read as zeros
-  __device__ __forceinline__ void load(const char* base, int64_t stride, int rows, int tid) {
-    const int r0 = tid / GR;
-    const char* p = base + r0 * stride + (tid % GR) * 16;
+typedef unsigned int ssm_u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int ssm_u32x4 __attribute__((ext_vector_type(4)));
+
+// A block's rows of one tensor, from its first row on: accesses past the last
+// row's end read zeros and write nothing (the hardware's range check).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t ssm_rows(const void* base, int64_t stride, int rows, int row_bytes) {
+  const uint32_t bytes = rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)stride + (uint32_t)row_bytes : 0u;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)bytes, 0x00027000);
+}
+
+template <typename TI>
+__device__ __forceinline__ void ssm_store4(__amdgpu_buffer_rsrc_t r, uint32_t offset, const f32x4& a) {
+  typename Quad<TI>::type v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = from_float<TI>(a[e]);
+  if constexpr (sizeof(TI) == 2)
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(ssm_u32x2, v), r, (int)offset, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(ssm_u32x4, v), r, (int)offset, 0, 0);
+}
+
+// s_waitcnt's immediate for vmcnt <= n alone.
+__host__ __device__ constexpr int ssm_vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
+template <int V>
+struct SsmInt {
+  static constexpr int value = V;
+};
+
+// Copies a block's rows of one tensor into a tile, granules swizzled (rows at
+// or after `rows` as zeros), straight to LDS, 1 KiB pieces over the waves.
+// Written as assembly so that the compiler does not wait for the copies at
+// every LDS read; the wave waits for them itself before the barrier that
+// hands them over.
+template <int ROWS, int GR, int NW>
+struct SsmCopy {
+  static constexpr int pieces = ROWS * GR / 64;
+  static constexpr int n = (pieces + NW - 1) / NW;  // a wave's, the last ones repeated
+  __device__ __forceinline__ static void issue(uint32_t tile, const char* base, int64_t stride, int rows, int wave,
+                                               int lane) {
+    rows = min(rows, ROWS);
+    ssm_u32x4 words;  // the buffer descriptor of ssm_rows
+    words[0] = (uint32_t)(uintptr_t)base;
+    words[1] = (uint32_t)((uintptr_t)base >> 32) & 0xffffu;
+    words[2] = rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)stride + (uint32_t)(GR * 16) : 0u;
+    words[3] = 0x00027000u;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r0 + i * rpi < rows) v[i] = ld16(p + i * rpi * stride);
-    }
-  }
-  // in the row's own order
-  __device__ __forceinline__ void store(char* tile, int tid) const {
-    const int g = tid % GR;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const int r = tid / GR + i * rpi;
-      if (r < ROWS) st16(tile + r * GR * 16 + ((g ^ ssm_swz<GR>(r)) * 16), v[i]);
-    }
-  }
-  // bf16 rows in k-tile order: the two quads of a granule to their lanes' units
-  __device__ __forceinline__ void store_ktile(char* tile, int tid) const {
-    const int g = tid % GR, k = 2 * (g & 1), o = ((g >> 1) & 1) * 8, u = (g >> 2) * 4;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const int r = tid / GR + i * rpi;
-      if (r >= ROWS) continue;
-      char* row = tile + r * GR * 16;
-      *(uint2*)(row + (((u + k) ^ ssm_swz<GR>(r)) * 16) + o) = make_uint2(v[i].x, v[i].y);
-      *(uint2*)(row + (((u + k + 1) ^ ssm_swz<GR>(r)) * 16) + o) = make_uint2(v[i].z, v[i].w);
+      const int piece = min(wave + i * NW, pieces - 1);
+      const int g = piece * 64 + lane, row = g / GR;
+      const uint32_t o = (uint32_t)row * (uint32_t)stride + (uint32_t)((g % GR) ^ ssm_swz<GR>(row)) * 16u;
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :
+                   : "s"(tile + piece * 1024), "v"(o), "s"(words)
+                   : "memory", "m0");
     }
   }
 };
@@ -237,40 +316,41 @@ __device__ __forceinline__ SsmSegment ssm_segment(const SsmParams& p, int s) {
   return g;
 }
 
-// Work item of a workgroup: XCD k (workgroups k, k + 8, ...) takes the k-th
-// eighth of the items in order, heads fastest, so that the heads that share
-// rows of b and c share an L2.
-__device__ __forceinline__ int64_t ssm_item(int64_t items) {
-  const int64_t per = (items + 7) / 8;
-  const int64_t i = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  return (blockIdx.x >> 3) < per && i < items ? i : -1;
+// A workgroup's segment and first head.  Workgroups k, k + 8, ... run on one
+// XCD: a unit of heads of one group and segment, which read the same rows of
+// b and c, goes to one of them (one L2), and the units go round them, so that
+// each has its share whatever number of the segments is real.
+struct SsmItem {
+  int seg, head;  // seg < 0: none
+};
+
+__device__ __forceinline__ SsmItem ssm_item(const SsmParams& p, int hp) {
+  const int hu = p.unit / hp, per_seg = p.heads / p.unit;  // workgroups of a unit, units of a segment
+  const int i = blockIdx.x >> 3;
+  const int64_t unit = (int64_t)(i / hu) * 8 + (blockIdx.x & 7);
+  SsmItem it;
+  it.seg = unit < (int64_t)p.max_segs * per_seg ? (int)(unit / per_seg) : -1;
+  it.head = (int)(unit % per_seg) * p.unit + (i % hu) * hp;
+  return it;
 }
 
 // OUT: the scan (c, y, states in and out); else a segment's end state.
-template <typename TI, int N, int P, bool OUT>
-__global__ __launch_bounds__((SsmShape<TI, N, P>::THREADS), 2) void ssm_kernel(SsmParams p) {
-  using D = SsmShape<TI, N, P>;
-  constexpr int C = D::C, NW = D::NW, CT = D::CT, RT = D::RT, NT = D::NT, NU = D::NU, TU = D::TU;
+template <typename TI, int N, int P, int HP, bool OUT>
+__global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI) == 2 ? 4 : 2)) void ssm_kernel(SsmParams p) {
+  using D = SsmShape<TI, N, P, HP, OUT>;
+  constexpr int C = D::C, NW = D::NW, NH = D::NH, CT = D::CT, RT = D::RT, NT = D::NT, NU = D::NU, TU = D::TU;
   constexpr int TPU = D::TPU, S = D::S;
   constexpr bool HALF = D::HALF;
   using U = typename Unit<TI>::type;
   __shared__ __attribute__((aligned(1024))) char smem[D::total];
-  char* const sB = smem + D::o_b;
-  char* const sC = smem + D::o_c;
-  char* const sX = smem + D::o_x;
-  char* const sM = smem + D::o_m;
-  char* const sL = smem + D::o_ml;
-  float* const s_cum = (float*)(smem + D::o_w);
-  float* const s_lo = s_cum + C;
-  float* const s_d = s_lo + C;
-  float* const s_w = s_d + C;
-  float* const s_e = s_w + C;
 
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, m = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t item = ssm_item((int64_t)p.max_segs * p.heads);
-  if (item < 0) return;
-  const int si = (int)(item / p.heads), h = (int)(item - (int64_t)si * p.heads);
+  const SsmItem item = ssm_item(p, HP);
+  if (item.seg < 0) return;
+  const int si = item.seg;
+  const int hh = wave / NH, wh = wave - hh * NH;  // the wave's head here, and its place in the head
+  const int h = item.head + hh;
   const int64_t state_elems = (int64_t)N * P;
 
   if (p.packed && si >= p.seg_off[p.n_seq]) {
@@ -282,43 +362,79 @@ __global__ __launch_bounds__((SsmShape<TI, N, P>::THREADS), 2) void ssm_kernel(S
     for (int i = si - total; i < p.n_seq; i += p.max_segs - total) {
       if (p.seg_off[i] != p.seg_off[i + 1]) continue;
       const int64_t o = ((int64_t)i * p.heads + h) * state_elems;
-      for (int e = tid; e < state_elems; e += D::THREADS) p.final_state[o + e] = p.init ? p.init[o + e] : 0.f;
+      for (int e = tid - hh * 64 * NH; e < state_elems; e += 64 * NH) p.final_state[o + e] = p.init ? p.init[o + e] : 0.f;
     }
     return;
   }
   const SsmSegment sg = ssm_segment(p, si);
   if (!OUT && sg.last) return;  // no later segment needs its end state
-
+  const int blocks = (sg.n + C - 1) / C;
+  // The copies: each turn asks for what the next turn needs (b and c two
+  // blocks ahead, since the next block's M is formed a block ahead; x one).
   const int grp = h / p.group;
-  const int64_t b_st = p.b_st * S, c_st = p.c_st * S, x_st = p.x_st * S;
+  const int64_t b_st = p.b_st * S, c_st = p.c_st * S, x_st = p.x_st * S, d_st = p.dt_st * 4;
   const char* pb = (const char*)p.b + sg.t0 * b_st + grp * p.b_sh * S;
-  const char* pc = (const char*)p.c + sg.t0 * c_st + grp * p.c_sh * S;
+  const char* pc = OUT ? (const char*)p.c + sg.t0 * c_st + grp * p.c_sh * S : nullptr;
   const char* px = (const char*)p.x + sg.t0 * x_st + h * p.x_sh * S;
-  const float* pd = p.dt + sg.t0 * p.dt_st + h * p.dt_sh;
-  TI* po = (TI*)p.out + sg.t0 * p.o_st + h * p.o_sh;
-  const float rate = -expf(p.a_log ? p.a_log[h] : 0.f) * kLog2e;
-  const float skip = OUT && p.d_skip ? p.d_skip[h] : 0.f;
-  const int col0 = wave * D::CW;
-
-  SsmLoad<C, D::GRB, D::THREADS> rb, rc;
-  SsmLoad<C, D::GRX, D::THREADS> rx;
-  float rd = 0.f;
-  auto fetch = [&](int t) {
-    const int rows = sg.n - t;
-    rb.load(pb + t * b_st, b_st, rows, tid);
-    if constexpr (OUT) rc.load(pc + t * c_st, c_st, rows, tid);
-    rx.load(px + t * x_st, x_st, rows, tid);
-    rd = 0.f;
-    if (wave == 0 && lane < C && lane < rows) rd = pd[(int64_t)(t + lane) * p.dt_st];
+  const char* pd = (const char*)(p.dt + sg.t0 * p.dt_st + h * p.dt_sh);
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  auto copy_bc = [&](int blk, int ring) {
+    const int t = blk * C;
+    SsmCopy<C, N * S / 16, NW>::issue(lds + ring * D::bc, pb + t * b_st, b_st, sg.n - t, wave, lane);
+    if constexpr (OUT)
+      SsmCopy<C, N * S / 16, NW>::issue(lds + ring * D::bc + D::BB, pc + t * c_st, c_st, sg.n - t, wave, lane);
   };
-  if (sg.n > 0) fetch(0);
+  auto copy_x = [&](int blk, int ring) {
+    const int t = blk * C;
+    SsmCopy<C, P * S / 16, NH>::issue(lds + D::o_x + (ring * HP + hh) * D::XB, px + t * x_st, x_st, sg.n - t, wh, lane);
+  };
+  // raw steps of blocks blk and blk + 1, one token a lane
+  auto fetch_steps = [&](int blk) {
+    const int t = blk * C;
+    const __amdgpu_buffer_rsrc_t r = ssm_rows(pd + t * d_st, d_st, min(sg.n - t, 2 * C), 4);
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, lane * (int)d_st, 0, 0));
+  };
+  const float rate = -expf(p.a_log ? p.a_log[h] : 0.f) * kLog2e;
+  const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+  // Steps d and decays of blocks blk and blk + 1 (tokens past the end have
+  // step 0).  In logarithms to base 2, with the sum run in fp64 (an fp32 sum
+  // of, say, -100 would leave 4e-6 in the difference of two neighbours):
+  //   c  sum of the token's own tile of 16 up to it,   E = 2^c,
+  //   f  d 2^(the tile's sum - c)
+  auto weigh = [&](int blk, float raw) {
+    const float d = blk * C + lane < sg.n ? ssm_step_size(bias, raw, p.softplus) : 0.f;
+    double c = (double)rate * (double)d;
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) {
+      const double o = __shfl_up(c, off, 16);
+      if ((lane & 15) >= off) c += o;
+    }
+    const double end = __shfl(c, 15, 16);
+    float* w = (float*)(smem + D::o_w + (((blk + (lane >> 5)) & (D::RW - 1)) * HP + hh) * D::WB) + (lane & 31);
+    w[0] = (float)c;
+    w[C] = d;
+    w[2 * C] = d * __builtin_amdgcn_exp2f((float)(end - c));
+    w[3 * C] = __builtin_amdgcn_exp2f((float)c);
+  };
+  // blocks asked for ahead of the one in use
+  constexpr int LB = D::RB - 1, LX = D::RX - 1;
+#pragma unroll
+  for (int i = 0; i < LB; ++i) {
+    copy_bc(i, i);
+    if (i < LX) copy_x(i, i);
+  }
+  // a wave's copies of a turn (without c)
+  constexpr int COPIES = SsmCopy<C, N * S / 16, NW>::n + SsmCopy<C, P * S / 16, NH>::n;
+  // pairs of blocks are weighed by the waves in turn
+  float raw = fetch_steps(2 * wh);
 
-  // the state before the segment: nt, ct tile, lane (q, m) holds rows
-  // 16 nt + 4 q + e of column col0 + 16 ct + m
+  // The state before the segment.  Tile (nt, ct), lane (q, m), element e:
+  // row ssm_state_row(nt, q) + e, column col0 + 16 ct + m.
+  const int col0 = wh * D::CW;
   f32x4 H[NT][CT];
   const int64_t so = ((int64_t)sg.seq * p.heads + h) * state_elems;
   float* slot = p.slots ? p.slots + ((int64_t)sg.slot * p.heads + h) * state_elems : nullptr;
-  const int fr = wave * NT * CT * 256 + lane * 4;  // a wave's fragments in a slot
+  const int fr = wh * NT * CT * 256 + lane * 4;  // a wave's fragments in a slot
   const bool from_slot = OUT && slot && !(sg.first && sg.last) && !(sg.first && !p.init);
   const float* from = sg.first && !from_slot ? p.init : nullptr;
 #pragma unroll
@@ -331,7 +447,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P>::THREADS), 2) void ssm_kernel(S
       } else if (from) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          H[nt][ct][e] = from[so + (int64_t)(16 * nt + 4 * q + e) * P + col0 + 16 * ct + m];
+          H[nt][ct][e] = from[so + (int64_t)(ssm_state_row<TI, N>(nt, q) + e) * P + col0 + 16 * ct + m];
       }
     }
   if (!OUT && sg.first && p.init) {
@@ -342,87 +458,105 @@ __global__ __launch_bounds__((SsmShape<TI, N, P>::THREADS), 2) void ssm_kernel(S
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) *(f32x4*)(slot + fr + (nt * CT + ct) * 256) = H[nt][ct];
   }
-  float total_log = 0.f;  // the segment's decay so far, base 2
-
-  for (int t = 0; t < sg.n; t += C) {
-    lds_barrier();  // the last block's readers are done
-    if constexpr (S == 2 && !HALF) {
-      rb.store_ktile(sB, tid);
-      if constexpr (OUT) rc.store_ktile(sC, tid);
-    } else {
-      rb.store(sB, tid);
-      if constexpr (OUT) rc.store(sC, tid);
-    }
-    rx.store(sX, tid);
-    if (wave == 0) {
-      // step sizes and their decays; rows past the end have step 0.  The sum
-      // runs in fp64 and is kept as two floats: an fp32 sum of, say, -100
-      // would leave 4e-6 in the difference of two neighbours
-      const float d = lane < sg.n - t && lane < C ? ssm_step_size(p.dt_bias, h, rd, p.softplus) : 0.f;
-      double cum = (double)rate * (double)d;
+  float skip = OUT && p.d_skip ? p.d_skip[h] : 0.f;
+  asm volatile("" : "+v"(skip));  // loaded here, not inside the loop
 #pragma unroll
-      for (int off = 1; off < C; off <<= 1) {
-        const double o = __shfl_up(cum, off);
-        if (lane >= off) cum += o;
-      }
-      const double last = __shfl(cum, C - 1);
-      if (lane < C) {
-        s_cum[lane] = (float)cum;
-        s_lo[lane] = (float)(cum - (double)(float)cum);
-        s_d[lane] = d;
-        s_w[lane] = d * __builtin_amdgcn_exp2f((float)(last - cum));
-        s_e[lane] = __builtin_amdgcn_exp2f((float)cum);
-      }
-    }
-    if (t + C < sg.n) fetch(t + C);
-    lds_barrier();
-    const float block_log = s_cum[C - 1];
-    const float alpha = s_e[C - 1];
-    total_log += block_log;
-
-    U xu[TU][CT];  // this wave's columns of x
-    if constexpr (OUT) {
-      // M's tiles (jt, it), jt <= it, over the waves: transposed products, so
-      // that lane (q, m) holds M[16 it + m][16 jt + 4 q + e], an operand's
-      // layout
-      for (int tile = wave; tile < RT * (RT + 1) / 2; tile += NW) {
-        const int it = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0;
-        const int jt = tile - it * (it + 1) / 2;
-        f32x4 acc = zero4();
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int u = 0; u < NU; ++u)
-          mma_unit<HALF>(acc, ssm_row_unit<TI, D::GRB, HALF>(sB, 16 * jt + m, u, q),
-                         ssm_row_unit<TI, D::GRB, HALF>(sC, 16 * it + m, u, q));
-        const f32x4 cj = *(const f32x4*)(s_cum + 16 * jt + 4 * q);
-        const f32x4 dj = *(const f32x4*)(s_d + 16 * jt + 4 * q);
-        const int i = 16 * it + m;
-        const f32x4 lj = *(const f32x4*)(s_lo + 16 * jt + 4 * q);
-        const float ci = s_cum[i], li = s_lo[i];
-        f32x4 hi, lo;
+    for (int ct = 0; ct < CT; ++ct) settle(H[nt][ct]);
+  // a state that is handed on takes three terms, one that only this segment
+  // reads two
+  const bool third = !OUT || (sg.last && p.final_state);
+  SsmRows<TI, N> rows(lane);
+  SsmCols<TI, P> cols(col0, lane);
+  uint32_t l8 = lane * 8;
+  const int64_t o_st = p.o_st * S;
+  char* po = (char*)p.out + sg.t0 * o_st + h * p.o_sh * S;
+  float decay = 1.f;  // the segment's so far
+  asm volatile("" : "+v"(l8));
+
+  // M of a block: transposed products, so that lane (q, m) holds M[16 it + m]
+  // [16 jt + 4 q + e], an operand's layout; one tile (0,0), (1,0), (1,1) a wave.
+  // bf16: the two terms of tile (0,0) as half units at 0 and 1536, of (1, jt)
+  // as the halves of full units at 512 and 2048; fp32: a unit per tile.
+  auto form_m = [&](const char* sB, const float* w, char* sM) {
+    const int q = l8 >> 7, m = (l8 >> 3) & 15;
+#pragma unroll 1
+    for (int tile = wh; tile < D::TILES; tile += NH) {
+      const int it = tile > 0, jt = tile > 1;
+      f32x4 acc = zero4();
+#pragma unroll
+      for (int u = 0; u < NU; ++u) mma_unit<HALF>(acc, rows.unit(sB, jt, u), rows.unit(sB + D::BB, it, u));
+      f32x4 v;
+      if (it == jt) {
+        const f32x4 cj = *(const f32x4*)(w + 16 * jt + 4 * q), dj = *(const f32x4*)(w + C + 16 * jt + 4 * q);
+        const float ci = w[16 * it + m];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = 16 * jt + 4 * q + e;
-          float v = j <= i ? acc[e] * __builtin_amdgcn_exp2f((ci - cj[e]) + (li - lj[e])) * dj[e] : 0.f;
-          if (j == i) v += skip;
-          hi[e] = v;
-          lo[e] = v - to_float(from_float<TI>(v));
+          const int j = 4 * q + e;
+          v[e] = acc[e] * (__builtin_amdgcn_exp2f(j <= m ? ci - cj[e] : -__builtin_inff()) * dj[e]) +
+                 (j == m ? skip : 0.f);
         }
-        int unit = 0;
+      } else {
+        // through the end of column tile 0, which lies between j and i
+        const f32x4 fj = *(const f32x4*)(w + 2 * C + 4 * q);
+        const float ei = w[3 * C + 16 + m];
 #pragma unroll
-        for (int i2 = 0; i2 < RT; ++i2)
-          if (i2 == it) unit = D::mu0(i2);
-        unit += jt / TPU;
-        const int o = unit * 1024 + lane * 16 + (TPU == 2 ? (jt & 1) * 8 : 0);
-        store4<TI>((TI*)(sM + o), hi[0], hi[1], hi[2], hi[3]);
-        if constexpr (S == 2) {
-          store4<TI>((TI*)(sL + o), lo[0], lo[1], lo[2], lo[3]);
-          if (jt == it && (it & 1) == 0) {  // the unit's second tile lies after the diagonal
-            *(uint2*)(sM + o + 8) = make_uint2(0u, 0u);
-            *(uint2*)(sL + o + 8) = make_uint2(0u, 0u);
-          }
-        }
+        for (int e = 0; e < 4; ++e) v[e] = acc[e] * fj[e] * ei;
       }
+      settle(v);
+      if constexpr (S == 4) {
+        *(f32x4*)(sM + tile * 1024 + l8 * 2) = v;
+      } else {
+        uint32_t p0[2], p1[2];
+        ssm_terms<2>(v[0], v[1], p0);
+        ssm_terms<2>(v[2], v[3], p1);
+        char* dst = sM + (it == 0 ? l8 : 512 + l8 * 2 + jt * 8);
+        *(uint2*)dst = make_uint2(p0[0], p1[0]);
+        *(uint2*)(dst + 1536) = make_uint2(p0[1], p1[1]);
+      }
+    }
+  };
 
+  if (wh == 0) {
+    weigh(0, raw);
+    raw = fetch_steps(2 * NH);
+  }
+  int rb = 0, rx = 0;
+  __builtin_amdgcn_s_waitcnt(ssm_vmcnt(0));  // (the copies, the raw steps)
+  if constexpr (OUT) {
+    lds_barrier();
+    form_m(smem, (const float*)(smem + D::o_w + hh * D::WB), smem + D::o_m + hh * D::MB);
+  }
+  for (int t = 0; t < blocks; ++t) {
+    // what this turn reads has landed: younger are the last turn's stores
+    // (OUT), or the copies of the last LB - 1 turns
+    __builtin_amdgcn_s_waitcnt(ssm_vmcnt(OUT ? RT * CT : (LB - 1) * COPIES));
+    lds_barrier();
+    copy_bc(t + LB, rb == 0 ? LB : rb - 1);
+    copy_x(t + LX, rx == 0 ? LX : rx - 1);
+    if ((t & 1) == 0 && ((t >> 1) + 1) % NH == wh) {
+      weigh(t + 2, raw);
+      raw = fetch_steps(t + 2 + 2 * NH);
+    }
+    // the places in the tiles, kept as they are: addresses derived from them
+    // outside the loop would take more registers than there are
+    asm volatile("" : "+v"(rows.row), "+v"(rows.col), "+v"(cols.at[0]), "+v"(l8));
+    const int q = l8 >> 7, m = (l8 >> 3) & 15;
+    const char* sB = smem + rb * D::bc;
+    const char* sX = smem + D::o_x + (rx * HP + hh) * D::XB;
+    const float* w = (const float*)(smem + D::o_w + ((t & (D::RW - 1)) * HP + hh) * D::WB);
+    rb = rb + 1 == D::RB ? 0 : rb + 1;
+    rx = rx + 1 == D::RX ? 0 : rx + 1;
+    const float e0 = w[3 * C + 15], e1 = w[3 * C + 31];
+    const float alpha = e0 * e1;
+    decay *= alpha;
+    U xu[TU][CT];  // this wave's columns of x
+#pragma unroll
+    for (int tu = 0; tu < TU; ++tu)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) xu[tu][ct] = cols.column(sX, ct, tu);
+    if constexpr (OUT) {
       // y^T tiles: rows are columns of x, columns are tokens
       f32x4 y[RT][CT];
 #pragma unroll
@@ -433,7 +567,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P>::THREADS), 2) void ssm_kernel(S
       for (int u = 0; u < NU; ++u) {
         U cu[RT];
 #pragma unroll
-        for (int it = 0; it < RT; ++it) cu[it] = ssm_row_unit<TI, D::GRB, HALF>(sC, 16 * it + m, u, q);
+        for (int it = 0; it < RT; ++it) cu[it] = rows.unit(sB + D::BB, it, u);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           if constexpr (S == 2) {
@@ -451,112 +585,134 @@ __global__ __launch_bounds__((SsmShape<TI, N, P>::THREADS), 2) void ssm_kernel(S
       }
 #pragma unroll
       for (int it = 0; it < RT; ++it) {
-        const float e = s_e[16 * it + m];
+        const float e = it == 0 ? w[3 * C + m] : w[3 * C + 16 + m] * e0;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
           for (int r = 0; r < 4; ++r) y[it][ct][r] *= e;
       }
+      const char* sM = smem + D::o_m + ((t & 1) * HP + hh) * D::MB;
+      if constexpr (S == 2) {
 #pragma unroll
-      for (int tu = 0; tu < TU; ++tu)
+        for (int k = 0; k < 2; ++k) {
+          const uint2 a = *(const uint2*)(sM + k * 1536 + l8);
+          const U m0 = __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, 0u, 0u));
+          const U m1 = *(const U*)(sM + k * 1536 + 512 + l8 * 2);
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) xu[tu][ct] = ssm_x_col<TI, P>(sX, col0 + 16 * ct, tu, lane);
-      lds_barrier();  // M is complete
-#pragma unroll
-      for (int it = 0; it < RT; ++it)
-#pragma unroll
-        for (int ju = 0; ju <= it / TPU; ++ju) {
-          const int o = (D::mu0(it) + ju) * 1024 + lane * 16;
-          const U mh = *(const U*)(sM + o);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) mma_unit<false>(y[it][ct], xu[ju][ct], mh);
-          if constexpr (S == 2) {
-            const U ml = *(const U*)(sL + o);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) mma_unit<false>(y[it][ct], xu[ju][ct], ml);
+          for (int ct = 0; ct < CT; ++ct) {
+            mma_unit<true>(y[0][ct], xu[0][ct], m0);
+            mma_unit<false>(y[1][ct], xu[0][ct], m1);
           }
         }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const U mk = *(const U*)(sM + k * 1024 + l8 * 2);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) mma_unit<false>(y[k > 0][ct], xu[k > 1 ? TU - 1 : 0][ct], mk);
+        }
+      }
+      const __amdgpu_buffer_rsrc_t dst = ssm_rows(po + (int64_t)t * C * o_st, o_st, min(sg.n - t * C, C), P * S);
 #pragma unroll
       for (int it = 0; it < RT; ++it) {
-        const int i = t + 16 * it + m;
+        const uint32_t o = (uint32_t)(16 * it + m) * (uint32_t)o_st + (uint32_t)(col0 + 4 * q) * S;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           settle(y[it][ct]);
-          if (i < sg.n)
-            store4<TI>(po + (int64_t)i * p.o_st + col0 + 16 * ct + 4 * q, y[it][ct][0], y[it][ct][1],
-                       y[it][ct][2], y[it][ct][3]);
+          ssm_store4<TI>(dst, o + 16 * ct * S, y[it][ct]);
         }
       }
-    } else {
+      // the next block's M
+      form_m(smem + rb * D::bc, (const float*)(smem + D::o_w + (((t + 1) & (D::RW - 1)) * HP + hh) * D::WB),
+             smem + D::o_m + (((t + 1) & 1) * HP + hh) * D::MB);
+    }
+
+    if constexpr (OUT) {
+      // read again: its registers serve the next block's M meanwhile
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int tu = 0; tu < TU; ++tu)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) xu[tu][ct] = ssm_x_col<TI, P>(sX, col0 + 16 * ct, tu, lane);
+        for (int ct = 0; ct < CT; ++ct) xu[tu][ct] = cols.column(sX, ct, tu);
     }
-
     // the state update
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) H[nt][ct][e] *= alpha;
-#pragma unroll
-    for (int tu = 0; tu < TU; ++tu) {
-      if constexpr (S == 2) {
-        const f32x4 w0 = *(const f32x4*)(s_w + 32 * tu + 4 * q);
-        const f32x4 w1 = *(const f32x4*)(s_w + 32 * tu + 16 + 4 * q);
-        bf16x8 a0[CT], a1[CT], a2[CT];
+    auto update = [&](auto terms) {
+      constexpr int TERMS = decltype(terms)::value;
+      auto age = [&](int tu, int nt) {  // before the tile's first product
+        if (tu > 0) return;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float v = (float)xu[tu][ct][e] * (e < 4 ? w0[e & 3] : w1[e & 3]);
-            a0[ct][e] = (bf16)v;
-            const float r = v - (float)a0[ct][e];
-            a1[ct][e] = (bf16)r;
-            a2[ct][e] = (bf16)(r - (float)a1[ct][e]);
+          for (int e = 0; e < 4; ++e) H[nt][ct][e] *= alpha;
+      };
+#pragma unroll
+      for (int tu = 0; tu < TU; ++tu) {
+        // w = d 2^(the block's sum - the sum up to the token)
+        f32x4 w0 = *(const f32x4*)(w + 2 * C + 16 * TPU * tu + 4 * q);
+        if (tu == 0) w0 *= e1;
+        if constexpr (S == 2) {
+          const f32x4 w1 = *(const f32x4*)(w + 2 * C + 16 + 4 * q);
+          bf16x8 a[TERMS][CT];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const uint4 x8 = __builtin_bit_cast(uint4, xu[tu][ct]);
+            const uint32_t x2[4] = {x8.x, x8.y, x8.z, x8.w};
+            uint32_t k[4][TERMS];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const f32x4& we = e < 2 ? w0 : w1;
+              ssm_terms<TERMS>(__uint_as_float(x2[e] << 16) * we[2 * (e & 1)],
+                               __uint_as_float(x2[e] & 0xffff0000u) * we[2 * (e & 1) + 1], k[e]);
+            }
+#pragma unroll
+            for (int i = 0; i < TERMS; ++i)
+              a[i][ct] = __builtin_bit_cast(bf16x8, make_uint4(k[0][i], k[1][i], k[2][i], k[3][i]));
           }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const U b = ssm_b_col<TI, N>(sB, nt, tu, lane);
+          for (int nt = 0; nt < NT; ++nt) {
+            const U b = rows.column(sB, nt, tu, l8 >> 3);
+            age(tu, nt);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) mma_unit<false>(H[nt][ct], b, a0[ct]);
+            for (int i = 0; i < TERMS; ++i)
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) mma_unit<false>(H[nt][ct], b, a1[ct]);
+              for (int ct = 0; ct < CT; ++ct) mma_unit<false>(H[nt][ct], b, a[i][ct]);
+          }
+        } else {
+          f32x4 a[CT];
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) mma_unit<false>(H[nt][ct], b, a2[ct]);
-        }
-      } else {
-        const f32x4 w = *(const f32x4*)(s_w + 16 * tu + 4 * q);
-        f32x4 a[CT];
+          for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+            for (int e = 0; e < 4; ++e) a[ct][e] = xu[tu][ct][e] * w0[e];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a[ct][e] = xu[tu][ct][e] * w[e];
+          for (int nt = 0; nt < NT; ++nt) {
+            const U b = rows.column(sB, nt, tu, l8 >> 3);
+            age(tu, nt);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const U b = ssm_b_col<TI, N>(sB, nt, tu, lane);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) mma_unit<false>(H[nt][ct], b, a[ct]);
+            for (int ct = 0; ct < CT; ++ct) mma_unit<false>(H[nt][ct], b, a[ct]);
+          }
         }
       }
-    }
+    };
+    if (!OUT || S == 4 || third) update(SsmInt<3>{});
+    else update(SsmInt<2>{});
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) settle(H[nt][ct]);
   }
 
+  __builtin_amdgcn_s_waitcnt(ssm_vmcnt(0));  // no copy may land after the workgroup's end
   if constexpr (OUT) {
     if (sg.last && p.final_state) {
+      asm volatile("" : "+v"(l8));
+      const int q = l8 >> 7, m = (l8 >> 3) & 15;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            p.final_state[so + (int64_t)(16 * nt + 4 * q + e) * P + col0 + 16 * ct + m] = H[nt][ct][e];
+            p.final_state[so + (int64_t)(ssm_state_row<TI, N>(nt, q) + e) * P + col0 + 16 * ct + m] = H[nt][ct][e];
     }
   } else {
     // into the next segment's slot
@@ -565,7 +721,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P>::THREADS), 2) void ssm_kernel(S
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) *(f32x4*)(dst + fr + (nt * CT + ct) * 256) = H[nt][ct];
-    if (tid == 0) p.seg_decay[(int64_t)sg.slot * p.heads + h] = __builtin_amdgcn_exp2f(total_log);
+    if (wh == 0 && lane == 0) p.seg_decay[(int64_t)sg.slot * p.heads + h] = decay;
   }
 }
 
@@ -586,14 +742,24 @@ __global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, 
   f32x4* v = (f32x4*)p.slots + ((int64_t)(s0 + 1) * p.heads + h) * vecs + (u - unit * vecs);
   const float* dec = p.seg_decay + (int64_t)(s0 + 1) * p.heads + h;
   f32x4 carry = *v;
-  for (int s = s0 + 2; s < s1; ++s) {
-    v += step;
-    const f32x4 e = *v;
-    const float d = *dec;
-    dec += p.heads;
+  // a batch of slots is asked for at once (past the last one it is read again)
+  constexpr int BATCH = 8;
+  for (int s = s0 + 2; s < s1; s += BATCH) {
+    f32x4 e[BATCH];
+    float d[BATCH];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) carry[i] = e[i] + d * carry[i];
-    *v = carry;
+    for (int i = 0; i < BATCH; ++i) {
+      const int k = min(s + i, s1 - 1) - (s0 + 1);
+      e[i] = v[k * step];
+      d[i] = dec[(int64_t)(k - 1) * p.heads];
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (s + i >= s1) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) carry[j] = e[i][j] + d[i] * carry[j];
+      v[(s + i - (s0 + 1)) * step] = carry;
+    }
   }
 }
 
@@ -629,7 +795,8 @@ __global__ __launch_bounds__((SsmStepShape<N, P>::NT)) void ssm_step_kernel(SsmS
   const TI* br = (const TI*)p.b + (int64_t)i * p.b_st + (int64_t)grp * p.b_sh + r0;
   const TI* cr = (const TI*)p.c + (int64_t)i * p.c_st + (int64_t)grp * p.c_sh + r0;
   const f32x4 x = load4<TI>((const TI*)p.x + (int64_t)i * p.x_st + (int64_t)h * p.x_sh + c0);
-  const float d = ssm_step_size(p.dt_bias, h, p.dt[(int64_t)i * p.dt_st + (int64_t)h * p.dt_sh], p.softplus);
+  const float d = ssm_step_size(p.dt_bias ? p.dt_bias[h] : 0.f, p.dt[(int64_t)i * p.dt_st + (int64_t)h * p.dt_sh],
+                                p.softplus);
   const float a = expf(-expf(p.a_log ? p.a_log[h] : 0.f) * d);
   f32x4 part = zero4();
 #pragma unroll
@@ -663,18 +830,35 @@ __global__ __launch_bounds__((SsmStepShape<N, P>::NT)) void ssm_step_kernel(SsmS
 
 int ssm_target_groups() { return 512; }
 
-template <typename TI, int N, int P>
-static hipError_t launch_ssm_np(bool out, const SsmParams& p, hipStream_t s) {
-  const int64_t items = (int64_t)p.max_segs * p.heads, blocks = (items + 7) / 8 * 8;
+template <typename TI, int N, int P, int HP>
+static hipError_t launch_ssm_kernel(bool out, const SsmParams& p, hipStream_t s) {
+  const int64_t units = (int64_t)p.max_segs * (p.heads / p.unit);
+  const int64_t blocks = (units + 7) / 8 * 8 * (p.unit / HP);
   if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), threads(SsmShape<TI, N, P>::THREADS);
-  if (out) {
-    hipLaunchKernelGGL((ssm_kernel<TI, N, P, true>), grid, threads, 0, s, p);
-    return hipGetLastError();
+  const dim3 grid((unsigned)blocks), threads(SsmShape<TI, N, P, HP, true>::THREADS);
+  if (out)
+    hipLaunchKernelGGL((ssm_kernel<TI, N, P, HP, true>), grid, threads, 0, s, p);
+  else
+    hipLaunchKernelGGL((ssm_kernel<TI, N, P, HP, false>), grid, threads, 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename TI, int N, int P>
+static hipError_t launch_ssm_np(bool out, const SsmParams& given, hipStream_t s) {
+  SsmParams p = given;
+  // heads that go to one XCD together: those of a group, unless that leaves
+  // XCDs without work
+  p.unit = (int64_t)p.max_segs * (p.heads / p.group) >= 64 ? p.group : 1;
+  hipError_t e;
+  // two heads of 64 columns fill a workgroup of eight waves
+  constexpr int HP = sizeof(TI) == 2 && P == 64 ? 2 : 1;
+  if (HP > 1 && p.group % HP == 0) {
+    p.unit = std::max(p.unit, HP);
+    e = launch_ssm_kernel<TI, N, P, HP>(out, p, s);
+  } else {
+    e = launch_ssm_kernel<TI, N, P, 1>(out, p, s);
   }
-  hipLaunchKernelGGL((ssm_kernel<TI, N, P, false>), grid, threads, 0, s, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (!p.packed && p.segs_per_seq < 3)) return e;
+  if (out || e != hipSuccess || (!p.packed && p.segs_per_seq < 3)) return e;
   const int vecs = N * P / 4;
   const int64_t join = ((int64_t)p.n_seq * p.heads * vecs + kSsmJoinThreads - 1) / kSsmJoinThreads;
   if (join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
