@@ -212,13 +212,26 @@ int ssm_options(const gdn_ssm_options* opts, gdn_ssm_options* o) {
 
 // Segments longer than this are cut (the chunk table counts in 32 bits).
 constexpr int64_t kMaxSegment = (int64_t)1 << 20;
-constexpr int64_t kMinAutoBlocks = 4;
+// Blocks per segment that spread the work over `groups` workgroups: of
+// uniform sequences, as many equal segments as make at most that many
+// workgroups; of packed ones, whose lengths the host does not know, an equal
+// share of all blocks.
+int64_t ssm_spread(const Ssm& P, int64_t groups) {
+  const int64_t block = gdn::kSsmBlock;
+  if (P.seq.packed) return (((P.T + block - 1) / block) * P.H + groups - 1) / groups;
+  const int64_t all = (P.seq.len + block - 1) / block;
+  const int64_t segs = std::max<int64_t>(1, groups / (P.H * P.seq.n));
+  return (all + segs - 1) / segs;
+}
 
 // Tokens per segment.  The automatic choice spreads the tokens x heads over
-// the workgroups that run at once, so that a few long sequences do not leave
-// the chip idle, in segments of at least four blocks: of uniform sequences,
-// as many equal segments as fit those workgroups in one round; of packed
-// ones, whose lengths the host does not know, an equal share of all blocks.
+// the two workgroups a compute unit holds, so that a few long sequences do
+// not leave the chip idle; problems too small for segments of four blocks
+// that way, over one workgroup a compute unit, in segments of two to four
+// blocks.  Measured: 4096 tokens x 16 heads (128 x 128 states) take 48 us in
+// segments of 4 blocks, 52 us in 2 or 3, 55 us in 6; 16384 x 48 heads 303 us
+// in 26 (the choice), 313 us in 13, 391 us in 43; 1000 tokens x 8 heads of
+// f32 39 us in 2, 56 us in 4.
 int64_t ssm_segment_tokens(const Ssm& P) {
   const int64_t block = gdn::kSsmBlock;
   int64_t blocks;
@@ -227,15 +240,9 @@ int64_t ssm_segment_tokens(const Ssm& P) {
   } else if (P.opts.segment_blocks < 0) {
     blocks = kMaxSegment / block;
   } else {
-    const int64_t target = gdn::ssm_target_groups();
-    if (P.seq.packed) {
-      blocks = (((P.T + block - 1) / block) * P.H + target - 1) / target;
-    } else {
-      const int64_t all = (P.seq.len + block - 1) / block;
-      const int64_t segs = std::max<int64_t>(1, target / (P.H * P.seq.n));
-      blocks = (all + segs - 1) / segs;
-    }
-    blocks = std::max(kMinAutoBlocks, blocks);
+    const int64_t full = gdn::ssm_target_groups();
+    blocks = ssm_spread(P, full);
+    if (blocks < 4) blocks = std::min<int64_t>(4, std::max<int64_t>(2, ssm_spread(P, full / 2)));
   }
   return std::min(blocks * block, kMaxSegment);
 }

@@ -202,6 +202,7 @@ __device__ __forceinline__ void ssm_terms(float a, float b, uint32_t (&t)[TERMS]
     v[1] = (bf16)b;
     t[i] = __builtin_bit_cast(uint32_t, v);
     if (i + 1 < TERMS) {
+      asm("" : "+v"(t[i]));  // unpacked again below, not rounded a second time
       a -= __uint_as_float(t[i] << 16);
       b -= __uint_as_float(t[i] & 0xffff0000u);
     }
@@ -416,15 +417,10 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     w[2 * C] = d * __builtin_amdgcn_exp2f((float)(end - c));
     w[3 * C] = __builtin_amdgcn_exp2f((float)c);
   };
-  // blocks asked for ahead of the one in use
-  constexpr int LB = D::RB - 1, LX = D::RX - 1;
-#pragma unroll
-  for (int i = 0; i < LB; ++i) {
-    copy_bc(i, i);
-    if (i < LX) copy_x(i, i);
-  }
-  // a wave's copies of a turn (without c)
-  constexpr int COPIES = SsmCopy<C, N * S / 16, NW>::n + SsmCopy<C, P * S / 16, NH>::n;
+  copy_bc(0, 0);
+  copy_bc(1, 1);
+  copy_x(0, 0);
+  if constexpr (!OUT) copy_x(1, 1);
   // pairs of blocks are weighed by the waves in turn
   float raw = fetch_steps(2 * wh);
 
@@ -529,12 +525,21 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     form_m(smem, (const float*)(smem + D::o_w + hh * D::WB), smem + D::o_m + hh * D::MB);
   }
   for (int t = 0; t < blocks; ++t) {
-    // what this turn reads has landed: younger are the last turn's stores
-    // (OUT), or the copies of the last LB - 1 turns
-    __builtin_amdgcn_s_waitcnt(ssm_vmcnt(OUT ? RT * CT : (LB - 1) * COPIES));
-    lds_barrier();
-    copy_bc(t + LB, rb == 0 ? LB : rb - 1);
-    copy_x(t + LX, rx == 0 ? LX : rx - 1);
+    if constexpr (OUT) {
+      // the last turn's copies have landed: only its stores are younger
+      __builtin_amdgcn_s_waitcnt(ssm_vmcnt(RT * CT));
+      lds_barrier();
+      copy_bc(t + 2, rb == 0 ? 2 : rb - 1);
+      copy_x(t + 1, rx ^ 1);
+    } else if ((t & 1) == 0) {
+      // two blocks a turn
+      __builtin_amdgcn_s_waitcnt(ssm_vmcnt(0));
+      lds_barrier();
+      copy_bc(t + 2, rb ^ 2);
+      copy_x(t + 2, rx ^ 2);
+      copy_bc(t + 3, rb ^ 3);
+      copy_x(t + 3, rx ^ 3);
+    }
     if ((t & 1) == 0 && ((t >> 1) + 1) % NH == wh) {
       weigh(t + 2, raw);
       raw = fetch_steps(t + 2 + 2 * NH);
