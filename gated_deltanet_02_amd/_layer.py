@@ -10,7 +10,6 @@ that the kernels run on.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import struct
 from typing import Optional
@@ -60,28 +59,27 @@ def _functions():
     return _fns
 
 
-def _describe(*named):
-    """Descriptors of the named tensors in one buffer, and the address of
-    each (None for None).  All tensors must be on one GPU."""
+def _describe(device, named):
+    """Descriptors of the named tensors in one buffer (kept by the caller
+    while it is used), and the address of each (None for None).  All tensors
+    must be on ``device``."""
     buf = ctypes.create_string_buffer(_DESC_BYTES * len(named))
     base = ctypes.addressof(buf)
-    at, device = [buf], None
-    for i, (name, t) in enumerate(named):
+    index = device.index
+    at = [buf]
+    for name, t in named:
         if t is None:
             at.append(None)
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-        n = t.dim()
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be a GPU tensor on {device} (got {t.device})")
+        shape = t.shape
+        n = len(shape)
         if not 1 <= n <= 4:
             raise ValueError(f"{name}: 1 to 4 dimensions")
-        _DESC[n].pack_into(buf, i * _DESC_BYTES, t.data_ptr(), _CODES.get(t.dtype, 0), n, *t.shape,
-                           *t.stride())
-        at.append(base + i * _DESC_BYTES)
+        off = (len(at) - 1) * _DESC_BYTES
+        _DESC[n].pack_into(buf, off, t.data_ptr(), _CODES.get(t.dtype, 0), n, *shape, *t.stride())
+        at.append(base + off)
     return at
 
 
@@ -91,24 +89,33 @@ def _vector(t: Optional[torch.Tensor], name: str, n: int, device):
         return None
     if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.get_device() != device.index:
+        raise ValueError(f"{name} must be a GPU tensor on {device} (got {t.device})")
     return t.data_ptr()
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Allocations and launches of the body belong to ``stream`` (default:
-    current) of ``device``; yields the stream's handle."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(x, stream, body):
+    """body(device, stream handle), with ``stream`` (default: the current
+    one of x's device) current: allocations and launches belong to it."""
+    device = x.device
     if device.type != "cuda":
         raise ValueError(f"x must be a GPU tensor (got {device})")
-    if stream is None:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
-    else:
+    if stream is not None:
         s = B._torch_stream(stream, device)
         with torch.cuda.stream(s):
-            yield s.cuda_stream
+            return body(device, s.cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        return body(device, _raw_stream(device.index))
+    with torch.cuda.device(device):
+        return body(device, _raw_stream(device.index))
+
+
+def _like(x):
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def gdn_ssm_default_options() -> GdnSsmOptions:
@@ -127,18 +134,21 @@ def gdn_short_conv(x, weight, bias=None, cu_seqlens=None, state_in=None, state_o
     (None: zeros) and its last rows (None: not written; may be
     ``state_in``).  Returns out."""
     L = _functions()
-    with _on(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        keep, px, pw, pc, pi, ps, po = _describe(
+
+    def body(device, handle):
+        y = _like(x) if out is None else out
+        keep, px, pw, pc, pi, ps, po = _describe(device, (
             ("x", x), ("weight", weight), ("cu_seqlens", cu_seqlens), ("state_in", state_in),
-            ("state_out", state_out), ("out", out))
-        pb = _vector(bias, "bias", x.shape[-1], x.device)
+            ("state_out", state_out), ("out", y)))
+        pb = _vector(bias, "bias", x.shape[-1], device)
         B._check(L.gdn_short_conv(px, pw, pb, pc, pi, ps, po, CONV_SILU if silu else 0, handle))
-    return out
+        return y
+
+    return _on(x, stream, body)
 
 
-def _ssm_options(a_log, dt_bias, d_skip, softplus, segment_blocks, heads, device):
+def _ssm_options(a_log, dt_bias, d_skip, softplus, segment_blocks, x, device):
+    heads = x.shape[-2] if x.dim() > 1 else 0
     o = GdnSsmOptions()
     o.a_log = _vector(a_log, "a_log", heads, device)
     o.dt_bias = _vector(dt_bias, "dt_bias", heads, device)
@@ -153,7 +163,7 @@ def gdn_ssm_workspace_size(x, b, cu_seqlens=None, segment_blocks: int = 0) -> in
     L = _functions()
     o = GdnSsmOptions()
     o.flags, o.segment_blocks = SSM_SOFTPLUS, segment_blocks
-    keep, px, pb, pc = _describe(("x", x), ("b", b), ("cu_seqlens", cu_seqlens))
+    keep, px, pb, pc = _describe(x.device, (("x", x), ("b", b), ("cu_seqlens", cu_seqlens)))
     n = ctypes.c_size_t(0)
     B._check(L.gdn_ssm_workspace_size(px, pb, pc, ctypes.addressof(o), ctypes.byref(n)))
     return n.value
@@ -177,26 +187,27 @@ def gdn_ssm_prefill(x, dt, b, c, a_log=None, dt_bias=None, d_skip=None, cu_seqle
     from ``ssm_workspace`` (allocated here if None).  Returns
     (out, final_state)."""
     L = _functions()
-    with _on(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        keep, px, pd, pb, pc, pq, pi, po, pf, _ = _describe(
+
+    def body(device, handle):
+        y, ws = _like(x) if out is None else out, workspace
+        keep, px, pd, pb, pc, pq, pi, po, pf, _ = _describe(device, (
             ("x", x), ("dt", dt), ("b", b), ("c", c), ("cu_seqlens", cu_seqlens),
-            ("init_state", init_state), ("out", out), ("final_state", final_state),
-            ("workspace", workspace))
-        o = _ssm_options(a_log, dt_bias, d_skip, softplus, segment_blocks, x.shape[-2] if x.dim() > 1 else 0,
-                         x.device)
-        po_opts = ctypes.addressof(o)
-        if workspace is None:
+            ("init_state", init_state), ("out", y), ("final_state", final_state),
+            ("workspace", ws)))
+        o = _ssm_options(a_log, dt_bias, d_skip, softplus, segment_blocks, x, device)
+        at = ctypes.addressof(o)
+        if ws is None:
             n = ctypes.c_size_t(0)
-            B._check(L.gdn_ssm_workspace_size(px, pb, pq, po_opts, ctypes.byref(n)))
+            B._check(L.gdn_ssm_workspace_size(px, pb, pq, at, ctypes.byref(n)))
             if n.value:
-                workspace = torch.empty(n.value, dtype=torch.uint8, device=x.device)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+                ws = torch.empty(n.value, dtype=torch.uint8, device=device)
+        elif ws.dtype != torch.uint8 or not ws.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor")
-        ws = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
-        B._check(L.gdn_ssm_prefill(px, pd, pb, pc, pq, pi, po, pf, po_opts, ws[0], ws[1], handle))
-    return out, final_state
+        where, size = (ws.data_ptr(), ws.numel()) if ws is not None else (None, 0)
+        B._check(L.gdn_ssm_prefill(px, pd, pb, pc, pq, pi, po, pf, at, where, size, handle))
+        return y, final_state
+
+    return _on(x, stream, body)
 
 
 def gdn_ssm_decode(x, dt, b, c, state, a_log=None, dt_bias=None, d_skip=None, out=None,
@@ -205,14 +216,16 @@ def gdn_ssm_decode(x, dt, b, c, state, a_log=None, dt_bias=None, d_skip=None, ou
     [N, H, n, p] is updated in place.  x [N, H, p]; dt f32 [N, H]; b, c
     [N, G, n].  Returns out [N, H, p]."""
     L = _functions()
-    with _on(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        keep, px, pd, pb, pc, ps, po = _describe(("x", x), ("dt", dt), ("b", b), ("c", c),
-                                                 ("state", state), ("out", out))
-        o = _ssm_options(a_log, dt_bias, d_skip, softplus, 0, x.shape[-2] if x.dim() > 1 else 0, x.device)
+
+    def body(device, handle):
+        y = _like(x) if out is None else out
+        keep, px, pd, pb, pc, ps, po = _describe(device, (
+            ("x", x), ("dt", dt), ("b", b), ("c", c), ("state", state), ("out", y)))
+        o = _ssm_options(a_log, dt_bias, d_skip, softplus, 0, x, device)
         B._check(L.gdn_ssm_decode(px, pd, pb, pc, ps, po, ctypes.addressof(o), handle))
-    return out
+        return y
+
+    return _on(x, stream, body)
 
 
 def gdn_add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, residual_out=None, out=None,
@@ -224,12 +237,14 @@ def gdn_add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, residual_
     nor ``out_q`` is.  residual_out and out may be x or residual.  Returns
     (out, residual_out, out_q, scales)."""
     L = _functions()
-    with _on(x.device, stream) as handle:
-        if out is None and out_q is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        keep, px, pr, pro, po, pq, ps = _describe(
-            ("x", x), ("residual", residual), ("residual_out", residual_out), ("out", out),
-            ("out_q", out_q), ("scales", scales))
-        pw = _vector(weight, "weight", x.shape[-1], x.device)
+
+    def body(device, handle):
+        y = _like(x) if out is None and out_q is None else out
+        keep, px, pr, pro, po, pq, ps = _describe(device, (
+            ("x", x), ("residual", residual), ("residual_out", residual_out), ("out", y),
+            ("out_q", out_q), ("scales", scales)))
+        pw = _vector(weight, "weight", x.shape[-1], device)
         B._check(L.gdn_add_rms_norm(px, pr, pw, eps, pro, po, pq, ps, handle))
-    return out, residual_out, out_q, scales
+        return y, residual_out, out_q, scales
+
+    return _on(x, stream, body)

@@ -4,6 +4,8 @@
 // to memory (small ones).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "gdn_device.h"
 #include "gdn_layer.h"
 
@@ -13,33 +15,27 @@ namespace gdn {
 // The short convolution: y[t, c] = bias[c] + sum_j w[c][j] e[t + j, c] (e: a
 // sequence's W - 1 history rows, then its rows), optionally silu.
 //
-// A thread takes 16 bytes' worth of adjacent channels and walks kConvTile
-// tokens with the last W - 1 rows in registers, so a row is read once per
-// tile plus W - 1 rows of overlap that neighbouring tiles find in L2.  The
-// tiles cut the tokens regardless of sequences and leave out each sequence's
-// first W - 1 tokens: those, and the new history, belong to one thread per
-// (sequence, channels) of the second kind of work item, the only one that
-// reads state_in and writes state_out, which may therefore be one array.
+// A thread takes 16 bytes' worth of adjacent channels (one element where
+// vector accesses do not fit) and walks a tile of 32 tokens, the last W - 1
+// rows in registers and the next four tokens' rows on their way, so a row is
+// read once, but for the W - 1 rows before a tile, which its neighbour on the
+// same XCD has in L2.  The taps lie channel by channel, 128 bytes apart for
+// neighbouring lanes: read as they lie they would take as long as a tile's
+// rows, so the workgroup reads them once in order and turns them in LDS.
+//
+// The tiles cut the tokens regardless of sequences and leave out each
+// sequence's first W - 1 tokens: those, and the new history, belong to a
+// second kind of work item, one per sequence, the only one that reads
+// state_in and writes state_out, which may therefore be one array.
 
 constexpr int kConvThreads = 256;
-constexpr int kConvTile = 16;
+constexpr int kConvTile = 32;
+constexpr int kConvGroup = 4;  // tokens asked for at once
 
 template <typename TI, bool VEC>
 struct ConvVec {
   static constexpr int n = VEC ? 16 / (int)sizeof(TI) : 1;
 };
-
-template <typename TI, bool VEC, int E>
-__device__ __forceinline__ void conv_load(float (&v)[E], const TI* p) {
-  if constexpr (VEC) {
-    const uint4 r = ld16(p);
-    const TI* e = (const TI*)&r;
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = to_float(e[i]);
-  } else {
-    v[0] = to_float(*p);
-  }
-}
 
 template <typename TI, bool VEC, int E>
 __device__ __forceinline__ void conv_store(TI* p, const float (&v)[E]) {
@@ -60,24 +56,57 @@ __device__ __forceinline__ int conv_cu(const ShortConvParams& p, int i) {
   return (int)min(max(e, (int64_t)0), (int64_t)p.t_total);
 }
 
+// What a thread loads of a row, and its values.
+template <typename TI, bool VEC>
+struct ConvRaw {
+  typename std::conditional<VEC, uint4, TI>::type v;
+  __device__ __forceinline__ void load(const TI* p) { v = *(const decltype(v)*)p; }
+  template <int E>
+  __device__ __forceinline__ void get(float (&f)[E]) const {
+    if constexpr (VEC) {
+      const TI* e = (const TI*)&v;
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = to_float(e[i]);
+    } else {
+      f[0] = to_float(v);
+    }
+  }
+};
+
+// A workgroup takes `cols` threads' channels (a power of two) of 256 / cols
+// work items; blocks_c workgroups cover the channels.
 template <typename TI, int W, bool VEC>
-__global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParams p, int tiles_per_seq,
-                                                                 int n_tiles) {
+__global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParams p, int cols, int blocks_c,
+                                                                 int tiles_per_seq, int n_tiles) {
   constexpr int E = ConvVec<TI, VEC>::n;
-  const int nvec = (p.d + E - 1) / E;
-  const int64_t u = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  const int item = (int)(u / nvec);
-  const int c0 = (int)(u - (int64_t)item * nvec) * E;
-  if (item >= n_tiles + p.n_seq) return;
+  __shared__ __attribute__((aligned(16))) float s_w[W + 1][kConvThreads * E];
+  // workgroups k, k + 8, ... run on one XCD: it takes an eighth of the work
+  // in order, so that neighbouring tiles share an L2
+  const unsigned per = (gridDim.x + 7) / 8, id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  const int cb = id % blocks_c, tx = threadIdx.x % cols;
+  const int64_t item64 = (int64_t)(id / blocks_c) * (kConvThreads / cols) + threadIdx.x / cols;
+  const int first = cb * cols * E;  // the workgroup's first channel
+  {
+    const int n = min(cols * E, p.d - first);
+    for (int i = threadIdx.x; i < n; i += kConvThreads) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) s_w[j][i] = p.w[(int64_t)(first + i) * W + j];
+      s_w[W][i] = p.bias ? p.bias[first + i] : 0.f;
+    }
+  }
+  __syncthreads();
+  const int c0 = first + tx * E;
+  if ((blockIdx.x >> 3) >= per || item64 >= (int64_t)n_tiles + p.n_seq || c0 >= p.d) return;
+  const int item = (int)item64;
   const TI* x = (const TI*)p.x + c0;
   TI* out = (TI*)p.out + c0;
 
   float w[W][E], bias[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    bias[e] = p.bias ? p.bias[c0 + e] : 0.f;
+    bias[e] = s_w[W][tx * E + e];
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][e] = p.w[(int64_t)(c0 + e) * W + j];
+    for (int j = 0; j < W; ++j) w[j][e] = s_w[j][tx * E + e];
   }
   // rows[j]: the raw row W - 1 - j tokens before the current one
   float rows[W][E];
@@ -122,22 +151,33 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
       t1 = min(t0 + kConvTile, end);
     }
     if (t0 >= t1) return;
+    ConvRaw<TI, VEC> before[W], next[kConvGroup];
 #pragma unroll
-    for (int j = 0; j + 1 < W; ++j) {
-      const int t = t0 - (W - 1) + j;
+    for (int j = 0; j + 1 < W; ++j) before[j].load(x + (int64_t)max(t0 - (W - 1) + j, 0) * p.x_st);
+    auto ask = [&](int t) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) rows[j][e] = 0.f;
-      if (t >= 0) conv_load<TI, VEC>(rows[j], x + (int64_t)t * p.x_st);
-    }
-    for (int t = t0; t < t1; ++t) {
-      while (t >= end && seq < last) {
-        ++seq;
-        start = conv_cu(p, seq);
-        end = conv_cu(p, seq + 1);
+      for (int i = 0; i < kConvGroup; ++i) next[i].load(x + (int64_t)min(t + i, t1 - 1) * p.x_st);
+    };
+    ask(t0);
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j) before[j].get(rows[j]);
+    for (int t = t0; t < t1; t += kConvGroup) {
+      ConvRaw<TI, VEC> now[kConvGroup];
+#pragma unroll
+      for (int i = 0; i < kConvGroup; ++i) now[i] = next[i];
+      ask(t + kConvGroup);
+#pragma unroll
+      for (int i = 0; i < kConvGroup; ++i) {
+        if (t + i >= t1) break;
+        while (t + i >= end && seq < last) {
+          ++seq;
+          start = conv_cu(p, seq);
+          end = conv_cu(p, seq + 1);
+        }
+        now[i].get(rows[W - 1]);
+        if (t + i - start >= W - 1) emit(t + i);
+        shift();
       }
-      conv_load<TI, VEC>(rows[W - 1], x + (int64_t)t * p.x_st);
-      if (t - start >= W - 1) emit(t);
-      shift();
     }
     return;
   }
@@ -153,59 +193,70 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
     len = p.seq_len;
   }
   const TI* hin = p.state_in ? (const TI*)p.state_in + (int64_t)seq * (W - 1) * p.d + c0 : nullptr;
-  float hist[W][E];
+  // everything it reads, asked for at once: the history, the first rows, the
+  // last rows (a row index clamped into the sequence where there is none)
+  ConvRaw<TI, VEC> hist[W], head[W], tail[W];
+#pragma unroll
+  for (int j = 0; j + 1 < W; ++j) {
+    if (hin) hist[j].load(hin + (int64_t)j * p.d);
+    if (len > 0) {
+      head[j].load(x + (int64_t)(start + min(j, len - 1)) * p.x_st);
+      tail[j].load(x + (int64_t)(start + max(len + j - (W - 1), 0)) * p.x_st);
+    }
+  }
 #pragma unroll
   for (int j = 0; j + 1 < W; ++j) {
 #pragma unroll
     for (int e = 0; e < E; ++e) rows[j][e] = 0.f;
-    if (hin) conv_load<TI, VEC>(rows[j], hin + (int64_t)j * p.d);
-#pragma unroll
-    for (int e = 0; e < E; ++e) hist[j][e] = rows[j][e];
+    if (hin) hist[j].get(rows[j]);
   }
+  float old[W][E];
+#pragma unroll
+  for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+    for (int e = 0; e < E; ++e) old[j][e] = rows[j][e];
 #pragma unroll
   for (int i = 0; i + 1 < W; ++i) {
     if (i < len) {
-      conv_load<TI, VEC>(rows[W - 1], x + (int64_t)(start + i) * p.x_st);
+      head[i].get(rows[W - 1]);
       emit(start + i);
       shift();
     }
   }
   if (!p.state_out) return;
   TI* hout = (TI*)p.state_out + (int64_t)seq * (W - 1) * p.d + c0;
-  float tail[W][E];
 #pragma unroll
   for (int j = 0; j + 1 < W; ++j) {
-    const int r = len + j;  // of the history followed by the sequence
-    if (r >= W - 1) {
-      conv_load<TI, VEC>(tail[j], x + (int64_t)(start + r - (W - 1)) * p.x_st);
-    } else {
+    // row len + j of the history followed by the sequence
+    float v[E];
 #pragma unroll
-      for (int k = 0; k + 1 < W; ++k)
-        if (k == r)
+    for (int k = 0; k + 1 < W; ++k)
+      if (k == len + j)
 #pragma unroll
-          for (int e = 0; e < E; ++e) tail[j][e] = hist[k][e];
-    }
+        for (int e = 0; e < E; ++e) v[e] = old[k][e];
+    if (len + j >= W - 1) tail[j].get(v);
+    conv_store<TI, VEC>(hout + (int64_t)j * p.d, v);
   }
-#pragma unroll
-  for (int j = 0; j + 1 < W; ++j) conv_store<TI, VEC>(hout + (int64_t)j * p.d, tail[j]);
 }
 
 template <typename TI, bool VEC>
 static hipError_t launch_short_conv_t(const ShortConvParams& p, hipStream_t s) {
   constexpr int E = ConvVec<TI, VEC>::n;
   const int64_t nvec = (p.d + E - 1) / E;
+  int cols = 1;
+  while (cols < nvec && cols < kConvThreads) cols *= 2;
+  const int64_t blocks_c = (nvec + cols - 1) / cols;
   // sequences of fewer than W tokens have no tokens for the tiles
   const int64_t per_seq = p.cu ? 0 : p.seq_len < p.width ? 0 : (p.seq_len + kConvTile - 1) / kConvTile;
   const int64_t tiles = p.cu ? ((int64_t)p.t_total + kConvTile - 1) / kConvTile : per_seq * p.n_seq;
-  const int64_t items = tiles + p.n_seq;
-  const int64_t blocks = (items * nvec + kConvThreads - 1) / kConvThreads;
+  const int64_t items = tiles + p.n_seq, per_block = kConvThreads / cols;
+  const int64_t blocks = ((items + per_block - 1) / per_block * blocks_c + 7) / 8 * 8;
   if (items >= ((int64_t)1 << 31) || blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  if (blocks == 0) return hipSuccess;
   switch (p.width) {
 #define GDN_CONV(W)                                                                                        \
     case W:                                                                                                \
       hipLaunchKernelGGL((short_conv_kernel<TI, W, VEC>), dim3((unsigned)blocks), dim3(kConvThreads), 0, s, p, \
-                         (int)per_seq, (int)tiles);                                                        \
+                         cols, (int)blocks_c, (int)per_seq, (int)tiles);                                   \
       return hipGetLastError();
     GDN_CONV(1) GDN_CONV(2) GDN_CONV(3) GDN_CONV(4)
 #undef GDN_CONV
