@@ -53,6 +53,14 @@ struct SsmParams {
   float* seg_decay;
 };
 
+// The segment table of a packed batch (see SsmParams).
+struct SsmTable {
+  const void* cu;   // [n_seq + 1] int32 or int64 (cu_i64)
+  int32_t* seg_off;
+  int32_t* table;
+  int32_t cu_i64, n_seq, t_total, seg_len, max_segs;
+};
+
 // gdn_ssm_decode.
 struct SsmStepParams {
   const void* x;
@@ -90,6 +98,7 @@ hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& p, hipStre
 constexpr int kSsmBlock = 64;
 // Workgroups the scan of a large problem is spread over.
 int ssm_target_groups();
+hipError_t launch_ssm_table(const SsmTable& p, hipStream_t s);
 // The segments' end states and their joining (only when sequences are cut),
 // then the scan.
 hipError_t launch_ssm_states(bool bf16, int n, int p, const SsmParams& sp, hipStream_t s);

@@ -29,8 +29,8 @@ namespace gdn {
 // state_in and writes state_out, which may therefore be one array.
 
 constexpr int kConvThreads = 256;
-constexpr int kConvTile = 32;
-constexpr int kConvGroup = 4;  // tokens asked for at once
+constexpr int kConvTile = 32;     // tokens per tile, fewer where tiles are few
+constexpr int kConvGroup = 4;     // tokens asked for at once
 
 template <typename TI, bool VEC>
 struct ConvVec {
@@ -76,7 +76,7 @@ struct ConvRaw {
 // A workgroup takes `cols` threads' channels (a power of two) of 256 / cols
 // work items; blocks_c workgroups cover the channels.
 template <typename TI, int W, bool VEC>
-__global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParams p, int cols, int blocks_c,
+__global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParams p, int cols, int blocks_c, int tile,
                                                                  int tiles_per_seq, int n_tiles) {
   constexpr int E = ConvVec<TI, VEC>::n;
   __shared__ __attribute__((aligned(16))) float s_w[W + 1][kConvThreads * E];
@@ -86,20 +86,53 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
   const int cb = id % blocks_c, tx = threadIdx.x % cols;
   const int64_t item64 = (int64_t)(id / blocks_c) * (kConvThreads / cols) + threadIdx.x / cols;
   const int first = cb * cols * E;  // the workgroup's first channel
+  const int c0 = first + tx * E;
+  const bool live = item64 < (int64_t)n_tiles + p.n_seq && c0 < p.d;
+  const int item = live ? (int)item64 : 0;
+  const TI* x = (const TI*)p.x + c0;
+  TI* out = (TI*)p.out + c0;
+  // What a sequence's own item reads, asked for before the taps are turned:
+  // the history, the first rows, the last rows.
+  const int own = live ? item - n_tiles : -1;  // its sequence, or < 0: a tile
+  int own_start = 0, own_len = 0;
+  ConvRaw<TI, VEC> hist[W], head[W], tail[W];
+  const TI* hin = nullptr;
+  if (own >= 0) {
+    if (p.cu) {
+      own_start = conv_cu(p, own);
+      own_len = max(conv_cu(p, own + 1) - own_start, 0);
+    } else {
+      own_start = own * p.seq_len;
+      own_len = p.seq_len;
+    }
+    if (p.state_in) hin = (const TI*)p.state_in + (int64_t)own * (W - 1) * p.d + c0;
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j) {
+      if (hin) hist[j].load(hin + (int64_t)j * p.d);
+      if (j < own_len) head[j].load(x + (int64_t)(own_start + j) * p.x_st);
+      if (own_len + j >= W - 1) tail[j].load(x + (int64_t)(own_start + own_len + j - (W - 1)) * p.x_st);
+    }
+  }
   {
     const int n = min(cols * E, p.d - first);
-    for (int i = threadIdx.x; i < n; i += kConvThreads) {
+    float t[E][W + 1];
 #pragma unroll
-      for (int j = 0; j < W; ++j) s_w[j][i] = p.w[(int64_t)(first + i) * W + j];
-      s_w[W][i] = p.bias ? p.bias[first + i] : 0.f;
+    for (int k = 0; k < E; ++k) {
+      const int i = min((int)threadIdx.x + k * kConvThreads, n - 1);
+#pragma unroll
+      for (int j = 0; j < W; ++j) t[k][j] = p.w[(int64_t)(first + i) * W + j];
+      t[k][W] = p.bias ? p.bias[first + i] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const int i = (int)threadIdx.x + k * kConvThreads;
+#pragma unroll
+      for (int j = 0; j <= W; ++j)
+        if (i < n) s_w[j][i] = t[k][j];
     }
   }
   __syncthreads();
-  const int c0 = first + tx * E;
-  if ((blockIdx.x >> 3) >= per || item64 >= (int64_t)n_tiles + p.n_seq || c0 >= p.d) return;
-  const int item = (int)item64;
-  const TI* x = (const TI*)p.x + c0;
-  TI* out = (TI*)p.out + c0;
+  if (!live) return;
 
   float w[W][E], bias[E];
 #pragma unroll
@@ -132,8 +165,8 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
     // tokens [t0, t1), the current sequence's start and end
     int t0, t1, start, end, seq = 0, last = 0;
     if (p.cu) {
-      t0 = item * kConvTile;
-      t1 = min(t0 + kConvTile, conv_cu(p, p.n_seq));
+      t0 = item * tile;
+      t1 = min(t0 + tile, conv_cu(p, p.n_seq));
       int lo = 0, hi = p.n_seq - 1;  // largest sequence starting at or before t0
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -147,8 +180,8 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
       seq = last = item / tiles_per_seq;
       start = seq * p.seq_len;
       end = start + p.seq_len;
-      t0 = start + (item - seq * tiles_per_seq) * kConvTile;
-      t1 = min(t0 + kConvTile, end);
+      t0 = start + (item - seq * tiles_per_seq) * tile;
+      t1 = min(t0 + tile, end);
     }
     if (t0 >= t1) return;
     ConvRaw<TI, VEC> before[W], next[kConvGroup];
@@ -183,27 +216,6 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
   }
 
   // A sequence's first W - 1 tokens and its new history.
-  const int seq = item - n_tiles;
-  int start, len;
-  if (p.cu) {
-    start = conv_cu(p, seq);
-    len = max(conv_cu(p, seq + 1) - start, 0);
-  } else {
-    start = seq * p.seq_len;
-    len = p.seq_len;
-  }
-  const TI* hin = p.state_in ? (const TI*)p.state_in + (int64_t)seq * (W - 1) * p.d + c0 : nullptr;
-  // everything it reads, asked for at once: the history, the first rows, the
-  // last rows (a row index clamped into the sequence where there is none)
-  ConvRaw<TI, VEC> hist[W], head[W], tail[W];
-#pragma unroll
-  for (int j = 0; j + 1 < W; ++j) {
-    if (hin) hist[j].load(hin + (int64_t)j * p.d);
-    if (len > 0) {
-      head[j].load(x + (int64_t)(start + min(j, len - 1)) * p.x_st);
-      tail[j].load(x + (int64_t)(start + max(len + j - (W - 1), 0)) * p.x_st);
-    }
-  }
 #pragma unroll
   for (int j = 0; j + 1 < W; ++j) {
 #pragma unroll
@@ -217,24 +229,24 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
     for (int e = 0; e < E; ++e) old[j][e] = rows[j][e];
 #pragma unroll
   for (int i = 0; i + 1 < W; ++i) {
-    if (i < len) {
+    if (i < own_len) {
       head[i].get(rows[W - 1]);
-      emit(start + i);
+      emit(own_start + i);
       shift();
     }
   }
   if (!p.state_out) return;
-  TI* hout = (TI*)p.state_out + (int64_t)seq * (W - 1) * p.d + c0;
+  TI* hout = (TI*)p.state_out + (int64_t)own * (W - 1) * p.d + c0;
 #pragma unroll
   for (int j = 0; j + 1 < W; ++j) {
     // row len + j of the history followed by the sequence
     float v[E];
 #pragma unroll
     for (int k = 0; k + 1 < W; ++k)
-      if (k == len + j)
+      if (k == own_len + j)
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = old[k][e];
-    if (len + j >= W - 1) tail[j].get(v);
+    if (own_len + j >= W - 1) tail[j].get(v);
     conv_store<TI, VEC>(hout + (int64_t)j * p.d, v);
   }
 }
@@ -246,9 +258,14 @@ static hipError_t launch_short_conv_t(const ShortConvParams& p, hipStream_t s) {
   int cols = 1;
   while (cols < nvec && cols < kConvThreads) cols *= 2;
   const int64_t blocks_c = (nvec + cols - 1) / cols;
+  // shorter tiles where the long ones would leave compute units with less
+  // than one workgroup each per SIMD (1237 rows of 1001 channels: 9.2 us in
+  // tiles of 32, 6.1 us in tiles of 8)
+  int tile = kConvTile;
+  while (tile > 2 * kConvGroup && (int64_t)p.t_total / tile * nvec < 1024 * kConvThreads) tile /= 2;
   // sequences of fewer than W tokens have no tokens for the tiles
-  const int64_t per_seq = p.cu ? 0 : p.seq_len < p.width ? 0 : (p.seq_len + kConvTile - 1) / kConvTile;
-  const int64_t tiles = p.cu ? ((int64_t)p.t_total + kConvTile - 1) / kConvTile : per_seq * p.n_seq;
+  const int64_t per_seq = p.cu ? 0 : p.seq_len < p.width ? 0 : (p.seq_len + tile - 1) / tile;
+  const int64_t tiles = p.cu ? ((int64_t)p.t_total + tile - 1) / tile : per_seq * p.n_seq;
   const int64_t items = tiles + p.n_seq, per_block = kConvThreads / cols;
   const int64_t blocks = ((items + per_block - 1) / per_block * blocks_c + 7) / 8 * 8;
   if (items >= ((int64_t)1 << 31) || blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
@@ -256,7 +273,7 @@ static hipError_t launch_short_conv_t(const ShortConvParams& p, hipStream_t s) {
 #define GDN_CONV(W)                                                                                        \
     case W:                                                                                                \
       hipLaunchKernelGGL((short_conv_kernel<TI, W, VEC>), dim3((unsigned)blocks), dim3(kConvThreads), 0, s, p, \
-                         cols, (int)blocks_c, (int)per_seq, (int)tiles);                                   \
+                         cols, (int)blocks_c, tile, (int)per_seq, (int)tiles);                                   \
       return hipGetLastError();
     GDN_CONV(1) GDN_CONV(2) GDN_CONV(3) GDN_CONV(4)
 #undef GDN_CONV

@@ -9,7 +9,6 @@
 
 #include "gdn.h"
 #include "gdn_api_common.h"
-#include "gdn_launch.h"
 #include "gdn_layer.h"
 
 namespace {
@@ -197,7 +196,7 @@ struct Ssm {
   gdn_ssm_options opts;
   int64_t seg_len = 0, segs_per_seq = 1, max_segs = 1;
   bool cut = false;  // some sequence may have two or more segments
-  size_t table = 0, seg_off = 0, seq_start = 0, slots = 0, decay = 0, total = 0;
+  size_t table = 0, seg_off = 0, slots = 0, decay = 0, total = 0;
 };
 
 int ssm_options(const gdn_ssm_options* opts, gdn_ssm_options* o) {
@@ -296,7 +295,6 @@ int ssm_sizes(const gdn_tensor* x, const gdn_tensor* b, const gdn_tensor* cu, co
   if (P->seq.packed) {
     P->table = take((size_t)P->max_segs * 16);
     P->seg_off = take((size_t)(P->seq.n + 1) * 4);
-    P->seq_start = take((size_t)(P->seq.n + 1) * 4);
   }
   if (P->cut) {
     P->decay = take((size_t)P->max_segs * P->H * 4);
@@ -464,7 +462,7 @@ int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor*
     }
   if ((rc = check_rows("out", P.T, P.o.st, P.H, out->stride[r - 2], P.P)) || (rc = token_stride("x", P.P, &P.x)) ||
       (rc = token_stride("b", P.N, &P.b)) || (rc = token_stride("c", P.N, &P.c)) ||
-      (rc = token_stride("out", P.P, &P.o)))
+      (rc = token_stride("out", P.P, &P.o)) || (rc = token_stride("dt", 1, &P.dt)))
     return rc;
   if (init_state && (rc = check_state(init_state, "init_state", P.seq.n, P))) return rc;
   if (final_state && (rc = check_state(final_state, "final_state", P.seq.n, P))) return rc;
@@ -514,17 +512,16 @@ int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor*
   if (P.seq.packed) {
     p.table = (const int32_t*)(base + P.table);
     p.seg_off = (const int32_t*)(base + P.seg_off);
-    gdn::TableParams tp{};
+    gdn::SsmTable tp{};
     tp.cu = cu_seqlens->data;
     tp.cu_i64 = cu_seqlens->dtype == GDN_DTYPE_I64 ? 1 : 0;
-    tp.seq_start = (int32_t*)(base + P.seq_start);
-    tp.chunk_off = (int32_t*)(base + P.seg_off);
+    tp.seg_off = (int32_t*)(base + P.seg_off);
     tp.table = (int32_t*)(base + P.table);
     tp.n_seq = P.seq.n;
     tp.t_total = (int32_t)P.T;
-    tp.chunk = (int32_t)P.seg_len;
-    tp.max_chunks = (int32_t)P.max_segs;
-    if ((e = gdn::launch_table(tp, s)) != hipSuccess)
+    tp.seg_len = (int32_t)P.seg_len;
+    tp.max_segs = (int32_t)P.max_segs;
+    if ((e = gdn::launch_ssm_table(tp, s)) != hipSuccess)
       return api_fail(GDN_ERR_HIP, "segment table launch: %s", hipGetErrorString(e));
   }
   if (P.cut) {

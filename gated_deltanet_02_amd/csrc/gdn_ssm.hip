@@ -393,7 +393,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
   auto fetch_steps = [&](int blk) {
     const int t = blk * C;
     const __amdgpu_buffer_rsrc_t r = ssm_rows(pd + t * d_st, d_st, min(sg.n - t, 2 * C), 4);
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, lane * (int)d_st, 0, 0));
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)((uint32_t)lane * (uint32_t)d_st), 0, 0));
   };
   const float rate = -expf(p.a_log ? p.a_log[h] : 0.f) * kLog2e;
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
@@ -730,21 +730,91 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
   }
 }
 
+// The segments of a packed batch: per segment a row (sequence, first token,
+// length, 0), and each sequence's first segment.  Ends are clamped into
+// [previous end, T], so that a malformed table can only give wrong results.
+// One workgroup, a sequence per thread and round, the scans over waves by
+// shuffles; each thread writes its own sequence's rows, or, of a sequence of
+// many segments, all threads do.
+constexpr int kSsmTableThreads = 1024;
+
+__global__ __launch_bounds__(kSsmTableThreads) void ssm_table_kernel(SsmTable p) {
+  __shared__ int s_end[16], s_sum[16], s_long[kSsmTableThreads][4], s_longs;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int carry_end = 0, carry = 0;  // of the rounds before
+  if (tid == 0) p.seg_off[0] = 0;
+  for (int base = 0; base < p.n_seq; base += kSsmTableThreads) {
+    const int i = base + tid;
+    int64_t e64 = 0;
+    if (i < p.n_seq) e64 = p.cu_i64 ? ((const int64_t*)p.cu)[i + 1] : ((const int32_t*)p.cu)[i + 1];
+    int end = (int)min(max(e64, (int64_t)0), (int64_t)p.t_total);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(end, off);
+      if (lane >= off) end = max(end, o);
+    }
+    if (lane == 63) s_end[wave] = end;
+    if (tid == 0) s_longs = 0;
+    __syncthreads();
+    int before = carry_end;  // the largest end of the waves before
+    for (int k = 0; k < wave; ++k) before = max(before, s_end[k]);
+    const int prev = __shfl_up(end, 1);
+    const int start = max(lane > 0 ? prev : 0, before);
+    end = max(end, before);
+    const int n = i < p.n_seq ? (end - start + p.seg_len - 1) / p.seg_len : 0;
+    int sum = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(sum, off);
+      if (lane >= off) sum += o;
+    }
+    if (lane == 63) s_sum[wave] = sum;
+    __syncthreads();
+    int first = carry;
+    for (int k = 0; k < 16; ++k) {
+      carry_end = max(carry_end, s_end[k]);
+      carry += s_sum[k];
+      if (k < wave) first += s_sum[k];
+    }
+    first += sum - n;
+    if (i < p.n_seq) p.seg_off[i + 1] = first + n;
+    auto row = [&](int seg, int seq, int from, int to, int k) {
+      if (seg >= p.max_segs) return;
+      const int t0 = from + k * p.seg_len;
+      *(int4*)(p.table + 4 * (int64_t)seg) = make_int4(seq, t0, min(p.seg_len, to - t0), 0);
+    };
+    if (n <= 4) {
+      for (int k = 0; k < n; ++k) row(first + k, i, start, end, k);
+    } else {
+      const int at = atomicAdd(&s_longs, 1);  // (the order does not matter)
+      s_long[at][0] = first;
+      s_long[at][1] = i;
+      s_long[at][2] = start;
+      s_long[at][3] = end;
+    }
+    __syncthreads();
+    for (int l = 0; l < s_longs; ++l) {
+      const int from = s_long[l][2], to = s_long[l][3];
+      for (int k = tid; k < (to - from + p.seg_len - 1) / p.seg_len; k += kSsmTableThreads)
+        row(s_long[l][0] + k, s_long[l][1], from, to, k);
+    }
+    __syncthreads();
+  }
+}
+
+hipError_t launch_ssm_table(const SsmTable& p, hipStream_t s) {
+  hipLaunchKernelGGL(ssm_table_kernel, dim3(1), dim3(kSsmTableThreads), 0, s, p);
+  return hipGetLastError();
+}
+
 // Joins a sequence's segments: the state before segment s is its
 // predecessor's end state plus the predecessor's decay times the state before
 // that one.  One thread per four elements of a (sequence, head) state.
 constexpr int kSsmJoinThreads = 256;
 
-__global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, int vecs) {
-  const int64_t u = (int64_t)blockIdx.x * kSsmJoinThreads + threadIdx.x;
-  const int64_t unit = u / vecs;
-  if (unit >= (int64_t)p.n_seq * p.heads) return;
-  const int seq = (int)(unit / p.heads), h = (int)(unit - (int64_t)seq * p.heads);
-  const int s0 = p.packed ? p.seg_off[seq] : seq * p.segs_per_seq;
-  const int s1 = p.packed ? p.seg_off[seq + 1] : s0 + p.segs_per_seq;
-  if (s1 - s0 < 3) return;
+__device__ __forceinline__ void ssm_join(const SsmParams& p, int s0, int s1, int h, int vecs, int at) {
   const int64_t step = (int64_t)p.heads * vecs;
-  f32x4* v = (f32x4*)p.slots + ((int64_t)(s0 + 1) * p.heads + h) * vecs + (u - unit * vecs);
+  f32x4* v = (f32x4*)p.slots + ((int64_t)(s0 + 1) * p.heads + h) * vecs + at;
   const float* dec = p.seg_decay + (int64_t)(s0 + 1) * p.heads + h;
   f32x4 carry = *v;
   // a batch of slots is asked for at once (past the last one it is read again)
@@ -766,6 +836,17 @@ __global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, 
       v[(s + i - (s0 + 1)) * step] = carry;
     }
   }
+}
+
+// `parts` workgroups share the vecs of one (sequence, head).
+__global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, int vecs, int parts) {
+  const int unit = blockIdx.x / parts, part = blockIdx.x - unit * parts;
+  const int seq = unit / p.heads, h = unit - seq * p.heads;
+  const int s0 = p.packed ? p.seg_off[seq] : seq * p.segs_per_seq;
+  const int s1 = p.packed ? p.seg_off[seq + 1] : s0 + p.segs_per_seq;
+  if (s1 - s0 < 3) return;
+  for (int at = part * kSsmJoinThreads + threadIdx.x; at < vecs; at += parts * kSsmJoinThreads)
+    ssm_join(p, s0, s1, h, vecs, at);
 }
 
 // ---------------------------------------------------------------------------
@@ -865,9 +946,13 @@ static hipError_t launch_ssm_np(bool out, const SsmParams& given, hipStream_t s)
   }
   if (out || e != hipSuccess || (!p.packed && p.segs_per_seq < 3)) return e;
   const int vecs = N * P / 4;
-  const int64_t join = ((int64_t)p.n_seq * p.heads * vecs + kSsmJoinThreads - 1) / kSsmJoinThreads;
-  if (join >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)join), dim3(kSsmJoinThreads), 0, s, p, vecs);
+  // workgroups for every vector; where that is many, most of them of packed
+  // sequences that are not cut, fewer that go round
+  const int64_t units = (int64_t)p.n_seq * p.heads;
+  const int all = (vecs + kSsmJoinThreads - 1) / kSsmJoinThreads;
+  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(all, 1024 / units));
+  if (units * parts >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(units * parts)), dim3(kSsmJoinThreads), 0, s, p, vecs, parts);
   return hipGetLastError();
 }
 
