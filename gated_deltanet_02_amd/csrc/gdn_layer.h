@@ -48,9 +48,11 @@ struct SsmParams {
   const int32_t* table;
   const int32_t* seg_off;
   // per segment and head: the state before the segment (fragment order, see
-  // gdn_ssm.hip) and the segment's whole decay; null when no sequence is cut
+  // gdn_ssm.hip) and the segment's whole decay, and per sequence and head the
+  // last segment's end state; null when no sequence is cut
   float* slots;
   float* seg_decay;
+  float* ends;
 };
 
 // The segment table of a packed batch (see SsmParams).

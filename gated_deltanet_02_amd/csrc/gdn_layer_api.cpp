@@ -196,7 +196,7 @@ struct Ssm {
   gdn_ssm_options opts;
   int64_t seg_len = 0, segs_per_seq = 1, max_segs = 1;
   bool cut = false;  // some sequence may have two or more segments
-  size_t table = 0, seg_off = 0, slots = 0, decay = 0, total = 0;
+  size_t table = 0, seg_off = 0, slots = 0, ends = 0, decay = 0, total = 0;
 };
 
 int ssm_options(const gdn_ssm_options* opts, gdn_ssm_options* o) {
@@ -299,6 +299,7 @@ int ssm_sizes(const gdn_tensor* x, const gdn_tensor* b, const gdn_tensor* cu, co
   if (P->cut) {
     P->decay = take((size_t)P->max_segs * P->H * 4);
     P->slots = take((size_t)P->max_segs * P->H * P->N * P->P * 4);
+    P->ends = take((size_t)P->seq.n * P->H * P->N * P->P * 4);
   }
   P->total = off;
   return GDN_OK;
@@ -527,6 +528,7 @@ int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor*
   if (P.cut) {
     p.slots = (float*)(base + P.slots);
     p.seg_decay = (float*)(base + P.decay);
+    p.ends = (float*)(base + P.ends);
     if ((e = gdn::launch_ssm_states(P.bf16, (int)P.N, (int)P.P, p, s)) != hipSuccess)
       return api_fail(GDN_ERR_HIP, "segment states launch: %s", hipGetErrorString(e));
   }

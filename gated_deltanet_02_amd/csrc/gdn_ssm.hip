@@ -368,7 +368,9 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     return;
   }
   const SsmSegment sg = ssm_segment(p, si);
-  if (!OUT && sg.last) return;  // no later segment needs its end state
+  // sequences of one segment need no state from here, and a last segment's
+  // end state only as the final state
+  if (!OUT && sg.last && (sg.first || !p.final_state)) return;
   const int blocks = (sg.n + C - 1) / C;
   // The copies: each turn asks for what the next turn needs (b and c two
   // blocks ahead, since the next block's M is formed a block ahead; x one).
@@ -462,7 +464,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     for (int ct = 0; ct < CT; ++ct) settle(H[nt][ct]);
   // a state that is handed on takes three terms, one that only this segment
   // reads two
-  const bool third = !OUT || (sg.last && p.final_state);
+  const bool third = !OUT || (sg.first && sg.last && p.final_state);
   SsmRows<TI, N> rows(lane);
   SsmCols<TI, P> cols(col0, lane);
   uint32_t l8 = lane * 8;
@@ -708,7 +710,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
 
   __builtin_amdgcn_s_waitcnt(ssm_vmcnt(0));  // no copy may land after the workgroup's end
   if constexpr (OUT) {
-    if (sg.last && p.final_state) {
+    if (sg.first && sg.last && p.final_state) {  // (of longer sequences the join writes it)
       asm volatile("" : "+v"(l8));
       const int q = l8 >> 7, m = (l8 >> 3) & 15;
 #pragma unroll
@@ -720,8 +722,8 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
             p.final_state[so + (int64_t)(ssm_state_row<TI, N>(nt, q) + e) * P + col0 + 16 * ct + m] = H[nt][ct][e];
     }
   } else {
-    // into the next segment's slot
-    float* dst = slot + (int64_t)p.heads * state_elems;
+    // into the next segment's slot, or the sequence's end
+    float* dst = sg.last ? p.ends + so : slot + (int64_t)p.heads * state_elems;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -809,44 +811,53 @@ hipError_t launch_ssm_table(const SsmTable& p, hipStream_t s) {
 
 // Joins a sequence's segments: the state before segment s is its
 // predecessor's end state plus the predecessor's decay times the state before
-// that one.  One thread per four elements of a (sequence, head) state.
+// that one; after the last, the final state.  A thread takes four elements of
+// a (sequence, head) state; `parts` workgroups share the vecs of one.
 constexpr int kSsmJoinThreads = 256;
 
-__device__ __forceinline__ void ssm_join(const SsmParams& p, int s0, int s1, int h, int vecs, int at) {
-  const int64_t step = (int64_t)p.heads * vecs;
-  f32x4* v = (f32x4*)p.slots + ((int64_t)(s0 + 1) * p.heads + h) * vecs + at;
-  const float* dec = p.seg_decay + (int64_t)(s0 + 1) * p.heads + h;
-  f32x4 carry = *v;
-  // a batch of slots is asked for at once (past the last one it is read again)
-  constexpr int BATCH = 8;
-  for (int s = s0 + 2; s < s1; s += BATCH) {
-    f32x4 e[BATCH];
-    float d[BATCH];
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int k = min(s + i, s1 - 1) - (s0 + 1);
-      e[i] = v[k * step];
-      d[i] = dec[(int64_t)(k - 1) * p.heads];
-    }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (s + i >= s1) break;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) carry[j] = e[i][j] + d[i] * carry[j];
-      v[(s + i - (s0 + 1)) * step] = carry;
-    }
-  }
-}
-
-// `parts` workgroups share the vecs of one (sequence, head).
-__global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, int vecs, int parts) {
+template <typename TI, int N, int P>
+__global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, int parts) {
+  constexpr int VECS = N * P / 4, NT = N / 16;
   const int unit = blockIdx.x / parts, part = blockIdx.x - unit * parts;
   const int seq = unit / p.heads, h = unit - seq * p.heads;
   const int s0 = p.packed ? p.seg_off[seq] : seq * p.segs_per_seq;
   const int s1 = p.packed ? p.seg_off[seq + 1] : s0 + p.segs_per_seq;
-  if (s1 - s0 < 3) return;
-  for (int at = part * kSsmJoinThreads + threadIdx.x; at < vecs; at += parts * kSsmJoinThreads)
-    ssm_join(p, s0, s1, h, vecs, at);
+  if (s1 - s0 < 2) return;
+  const int64_t step = (int64_t)p.heads * VECS;
+  for (int at = part * kSsmJoinThreads + threadIdx.x; at < VECS; at += parts * kSsmJoinThreads) {
+    f32x4* v = (f32x4*)p.slots + ((int64_t)(s0 + 1) * p.heads + h) * VECS + at;
+    const float* dec = p.seg_decay + (int64_t)(s0 + 1) * p.heads + h;
+    f32x4 end = zero4();
+    if (p.final_state) end = ((const f32x4*)p.ends)[(int64_t)unit * VECS + at];
+    const float last = dec[(int64_t)(s1 - s0 - 2) * p.heads];
+    f32x4 carry = *v;
+    // a batch of slots is asked for at once (past the last one it is read again)
+    constexpr int BATCH = 8;
+    for (int s = s0 + 2; s < s1; s += BATCH) {
+      f32x4 e[BATCH];
+      float d[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int k = min(s + i, s1 - 1) - (s0 + 1);
+        e[i] = v[k * step];
+        d[i] = dec[(int64_t)(k - 1) * p.heads];
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        if (s + i >= s1) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) carry[j] = e[i][j] + d[i] * carry[j];
+        v[(s + i - (s0 + 1)) * step] = carry;
+      }
+    }
+    if (p.final_state) {
+      // the fragment's place in the state (see ssm_kernel): wave's columns, tile, lane
+      const int lane = at & 63, nt = (at >> 6) % NT, wave = (at >> 6) / NT;
+      float* dst = p.final_state + ((int64_t)unit * N + ssm_state_row<TI, N>(nt, lane >> 4)) * P + 16 * wave + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dst[j * P] = end[j] + last * carry[j];
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -944,15 +955,15 @@ static hipError_t launch_ssm_np(bool out, const SsmParams& given, hipStream_t s)
   } else {
     e = launch_ssm_kernel<TI, N, P, 1>(out, p, s);
   }
-  if (out || e != hipSuccess || (!p.packed && p.segs_per_seq < 3)) return e;
-  const int vecs = N * P / 4;
+  if (out || e != hipSuccess) return e;
   // workgroups for every vector; where that is many, most of them of packed
   // sequences that are not cut, fewer that go round
   const int64_t units = (int64_t)p.n_seq * p.heads;
-  const int all = (vecs + kSsmJoinThreads - 1) / kSsmJoinThreads;
+  const int all = (N * P / 4 + kSsmJoinThreads - 1) / kSsmJoinThreads;
   const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(all, 1024 / units));
   if (units * parts >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)(units * parts)), dim3(kSsmJoinThreads), 0, s, p, vecs, parts);
+  hipLaunchKernelGGL((ssm_join_kernel<TI, N, P>), dim3((unsigned)(units * parts)), dim3(kSsmJoinThreads), 0, s, p,
+                     parts);
   return hipGetLastError();
 }
 

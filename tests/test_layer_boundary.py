@@ -165,9 +165,10 @@ def wsize(lib, T, H, G, N, P, cu=None, o=None, dt=BF16):
 def test_scan_workspace(lib):
     assert wsize(lib, 100, 4, 2, 64, 32) == 0                      # a short sequence: one pass
     assert wsize(lib, 100000, 4, 2, 64, 32, o=opts(segment_blocks=-1)) == 0
-    # segments of one block: a decay and a state per segment and head
+    # segments of one block: a decay and a state per segment and head, and the
+    # end of each sequence and head
     got = wsize(lib, 640, 4, 2, 64, 32, o=opts(segment_blocks=1))
-    assert got == 256 + 10 * 4 * 64 * 32 * 4
+    assert got == 256 + (10 + 1) * 4 * 64 * 32 * 4
     # packed: the table and the segments' offsets besides
     got = wsize(lib, 640, 4, 2, 64, 32, cu=fake((4,), I32), o=opts(segment_blocks=-1))
     assert got == 256 + 256
