@@ -36,6 +36,10 @@ class GdnSsmOptions(ctypes.Structure):
                 ("segment_blocks", ctypes.c_int32)]
 
 
+_OPTIONS = struct.Struct("=QQQIi")  # the same, packed
+assert _OPTIONS.size == ctypes.sizeof(GdnSsmOptions)
+
+
 _fns = None
 
 
@@ -61,9 +65,9 @@ def _functions():
 
 def _describe(device, named):
     """Descriptors of the named tensors in one buffer (kept by the caller
-    while it is used), and the address of each (None for None).  All tensors
-    must be on ``device``."""
-    buf = ctypes.create_string_buffer(_DESC_BYTES * len(named))
+    while it is used; room for the scan's options at its end), and the
+    address of each (None for None).  All tensors must be on ``device``."""
+    buf = (ctypes.c_char * (_DESC_BYTES * len(named) + _OPTIONS.size))()
     base = ctypes.addressof(buf)
     index = device.index
     at = [buf]
@@ -87,7 +91,7 @@ def _vector(t: Optional[torch.Tensor], name: str, n: int, device):
     """Address of an f32 vector of n values (None -> NULL)."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values")
     if t.get_device() != device.index:
         raise ValueError(f"{name} must be a GPU tensor on {device} (got {t.device})")
@@ -96,6 +100,7 @@ def _vector(t: Optional[torch.Tensor], name: str, n: int, device):
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on(x, stream, body):
@@ -108,13 +113,15 @@ def _on(x, stream, body):
         s = B._torch_stream(stream, device)
         with torch.cuda.stream(s):
             return body(device, s.cuda_stream)
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:  # (x is on a GPU: torch has initialised it)
         return body(device, _raw_stream(device.index))
     with torch.cuda.device(device):
         return body(device, _raw_stream(device.index))
 
 
 def _like(x):
+    if x.is_contiguous():
+        return torch.empty_like(x)
     return torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
@@ -147,15 +154,14 @@ def gdn_short_conv(x, weight, bias=None, cu_seqlens=None, state_in=None, state_o
     return _on(x, stream, body)
 
 
-def _ssm_options(a_log, dt_bias, d_skip, softplus, segment_blocks, x, device):
+def _ssm_options(keep, a_log, dt_bias, d_skip, softplus, segment_blocks, x, device):
+    """Packs the options behind the descriptors in ``keep``; their address."""
     heads = x.shape[-2] if x.dim() > 1 else 0
-    o = GdnSsmOptions()
-    o.a_log = _vector(a_log, "a_log", heads, device)
-    o.dt_bias = _vector(dt_bias, "dt_bias", heads, device)
-    o.d_skip = _vector(d_skip, "d_skip", heads, device)
-    o.flags = SSM_SOFTPLUS if softplus else 0
-    o.segment_blocks = segment_blocks
-    return o
+    off = len(keep) - _OPTIONS.size
+    _OPTIONS.pack_into(keep, off, _vector(a_log, "a_log", heads, device) or 0,
+                       _vector(dt_bias, "dt_bias", heads, device) or 0, _vector(d_skip, "d_skip", heads, device) or 0,
+                       SSM_SOFTPLUS if softplus else 0, segment_blocks)
+    return ctypes.addressof(keep) + off
 
 
 def gdn_ssm_workspace_size(x, b, cu_seqlens=None, segment_blocks: int = 0) -> int:
@@ -194,8 +200,7 @@ def gdn_ssm_prefill(x, dt, b, c, a_log=None, dt_bias=None, d_skip=None, cu_seqle
             ("x", x), ("dt", dt), ("b", b), ("c", c), ("cu_seqlens", cu_seqlens),
             ("init_state", init_state), ("out", y), ("final_state", final_state),
             ("workspace", ws)))
-        o = _ssm_options(a_log, dt_bias, d_skip, softplus, segment_blocks, x, device)
-        at = ctypes.addressof(o)
+        at = _ssm_options(keep, a_log, dt_bias, d_skip, softplus, segment_blocks, x, device)
         if ws is None:
             n = ctypes.c_size_t(0)
             B._check(L.gdn_ssm_workspace_size(px, pb, pq, at, ctypes.byref(n)))
@@ -221,8 +226,8 @@ def gdn_ssm_decode(x, dt, b, c, state, a_log=None, dt_bias=None, d_skip=None, ou
         y = _like(x) if out is None else out
         keep, px, pd, pb, pc, ps, po = _describe(device, (
             ("x", x), ("dt", dt), ("b", b), ("c", c), ("state", state), ("out", y)))
-        o = _ssm_options(a_log, dt_bias, d_skip, softplus, 0, x, device)
-        B._check(L.gdn_ssm_decode(px, pd, pb, pc, ps, po, ctypes.addressof(o), handle))
+        at = _ssm_options(keep, a_log, dt_bias, d_skip, softplus, 0, x, device)
+        B._check(L.gdn_ssm_decode(px, pd, pb, pc, ps, po, at, handle))
         return y
 
     return _on(x, stream, body)

@@ -9,6 +9,9 @@
 
 namespace gdn {
 
+// A launch has fewer than 2^32 threads.
+constexpr int64_t kLaunchThreads = ((int64_t)1 << 32) - 1;
+
 // gdn_short_conv.
 struct ShortConvParams {
   const void* x;         // [T, D], token stride x_st, unit channel stride

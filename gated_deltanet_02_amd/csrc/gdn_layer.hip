@@ -23,6 +23,11 @@ namespace gdn {
 // neighbouring lanes: read as they lie they would take as long as a tile's
 // rows, so the workgroup reads them once in order and turns them in LDS.
 //
+// Measured (bf16, W = 4): 137k tokens x 6144 channels 666 us, 5.1 TB/s (a
+// large copy reaches 4.8; 984 us in tiles of 64 with the taps read as they lie
+// and no rows on their way); 256 steps of 6144 channels 9.0 us, the launch and
+// the trips for the table, the rows and the taps.
+//
 // The tiles cut the tokens regardless of sequences and leave out each
 // sequence's first W - 1 tokens: those, and the new history, belong to a
 // second kind of work item, one per sequence, the only one that reads
@@ -268,7 +273,7 @@ static hipError_t launch_short_conv_t(const ShortConvParams& p, hipStream_t s) {
   const int64_t tiles = p.cu ? ((int64_t)p.t_total + tile - 1) / tile : per_seq * p.n_seq;
   const int64_t items = tiles + p.n_seq, per_block = kConvThreads / cols;
   const int64_t blocks = ((items + per_block - 1) / per_block * blocks_c + 7) / 8 * 8;
-  if (items >= ((int64_t)1 << 31) || blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  if (items >= ((int64_t)1 << 31) || blocks > kLaunchThreads / kConvThreads) return hipErrorInvalidValue;
   switch (p.width) {
 #define GDN_CONV(W)                                                                                        \
     case W:                                                                                                \
@@ -295,7 +300,10 @@ hipError_t launch_short_conv(bool bf16, bool vec, const ShortConvParams& p, hipS
 // columns, so the row is read once and the two reductions (the sum of
 // squares; the largest |y|, of a row, or of the 16 lanes that hold a group)
 // run on registers.  Rows of up to 1024 columns take one wave each, longer
-// ones a workgroup.
+// ones a workgroup.  Measured: 4096 rows of 5120 columns in bf16 with residual
+// and both outputs 44 us, 4.3 TB/s; 131071 rows of 6144 with 8-bit output
+// alone 994 us, 5.7 TB/s; eight rows 3.9 us, the launch, one trip and the
+// reductions.
 
 constexpr int kNormVec = 8;
 constexpr float kE4m3Max = 448.f;
@@ -478,7 +486,6 @@ static hipError_t launch_add_rms_norm_t(const NormParams& p, hipStream_t s) {
   const int vecs = (p.d + kNormVec - 1) / kNormVec;
   const bool wave = vecs <= 128;
   const int64_t blocks = wave ? (p.rows + 3) / 4 : p.rows;
-  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
 #define GDN_NORM(TPR, NV)                                                                             \
   do {                                                                                                \
     hipLaunchKernelGGL((add_rms_norm_kernel<TI, TPR, NV, VEC>), dim3((unsigned)blocks),                \
@@ -498,10 +505,25 @@ static hipError_t launch_add_rms_norm_t(const NormParams& p, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& p, hipStream_t s) {
-  if (p.rows <= 0) return hipSuccess;
-  if (bf16) return vec ? launch_add_rms_norm_t<gdn::bf16, true>(p, s) : launch_add_rms_norm_t<gdn::bf16, false>(p, s);
-  return vec ? launch_add_rms_norm_t<float, true>(p, s) : launch_add_rms_norm_t<float, false>(p, s);
+hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& all, hipStream_t s) {
+  const int64_t size = bf16 ? 2 : 4;
+  constexpr int64_t most = (int64_t)1 << 21;  // rows of a launch, a row taking at most 1024 threads
+  for (int64_t row = 0; row < all.rows; row += most) {
+    NormParams p = all;
+    auto at = [&](auto* a, int64_t bytes) { return a ? (decltype(a))((uintptr_t)a + row * bytes) : a; };
+    p.rows = all.rows - row < most ? all.rows - row : most;
+    p.x = at(all.x, all.x_st * size);
+    p.res = at(all.res, all.r_st * size);
+    p.res_out = at(all.res_out, all.ro_st * size);
+    p.out = at(all.out, all.o_st * size);
+    p.out_q = at(all.out_q, all.q_st);
+    p.scales = at(all.scales, (all.groups ? all.groups : 1) * 4);
+    const hipError_t e =
+        bf16 ? (vec ? launch_add_rms_norm_t<gdn::bf16, true>(p, s) : launch_add_rms_norm_t<gdn::bf16, false>(p, s))
+             : (vec ? launch_add_rms_norm_t<float, true>(p, s) : launch_add_rms_norm_t<float, false>(p, s));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace gdn

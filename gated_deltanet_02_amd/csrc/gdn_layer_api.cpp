@@ -16,7 +16,11 @@ namespace {
 using gdn::api_fail;
 
 constexpr int64_t kMax32 = (int64_t)1 << 31;
+// Tokens, sequences and channels: the kernels' 32-bit counters may run past
+// the last one by a tile, a segment or a round of threads.
+constexpr int64_t kMaxCount = kMax32 - ((int64_t)1 << 21);
 constexpr int64_t kMaxElements = (int64_t)1 << 48;
+constexpr int64_t kMaxThreads = (int64_t)1 << 32;  // of one launch
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
@@ -126,7 +130,7 @@ int parse_tokens(const gdn_tensor* t, const char* name, int rank, Tokens* v) {
   v->T = batched ? t->shape[0] * t->shape[1] : t->shape[0];
   v->st = t->stride[batched ? 1 : 0];
   if (batched && t->shape[1] == 1) v->st = t->stride[0];
-  if (v->T >= kMax32) return api_fail(GDN_ERR_SHAPE, "%s: T must be < 2^31", name);
+  if (v->T > kMaxCount) return api_fail(GDN_ERR_SHAPE, "%s: T must be at most 2^31 - 2^21", name);
   if (batched && !is_empty(t) && t->shape[0] > 1 && t->shape[1] > 1 && t->stride[0] != t->shape[1] * t->stride[1])
     return api_fail(GDN_ERR_LAYOUT, "%s: batch stride must equal seq_len * token stride", name);
   return GDN_OK;
@@ -142,7 +146,7 @@ struct Sequences {
 int parse_sequences(const gdn_tensor* cu, int64_t batch, int64_t tokens, Sequences* s) {
   if (!cu) {
     if (batch < 1) return api_fail(GDN_ERR_SHAPE, "at least one sequence is required");
-    if (batch >= kMax32) return api_fail(GDN_ERR_SHAPE, "too many sequences");
+    if (batch > kMaxCount) return api_fail(GDN_ERR_SHAPE, "too many sequences");
     s->packed = false;
     s->n = (int)batch;
     s->len = (int)(tokens / batch);
@@ -151,7 +155,7 @@ int parse_sequences(const gdn_tensor* cu, int64_t batch, int64_t tokens, Sequenc
   if (cu->dtype != GDN_DTYPE_I32 && cu->dtype != GDN_DTYPE_I64)
     return api_fail(GDN_ERR_DTYPE, "cu_seqlens must be int32 or int64");
   if (cu->ndim != 1 || cu->shape[0] < 2) return api_fail(GDN_ERR_SHAPE, "cu_seqlens must be 1-D with N+1 >= 2 entries");
-  if (cu->shape[0] - 1 >= kMax32) return api_fail(GDN_ERR_SHAPE, "too many sequences");
+  if (cu->shape[0] - 1 > kMaxCount) return api_fail(GDN_ERR_SHAPE, "too many sequences");
   if (cu->stride[0] != 1) return api_fail(GDN_ERR_LAYOUT, "cu_seqlens must be contiguous");
   if (!cu->data) return api_fail(GDN_ERR_NULL_ARG, "cu_seqlens data is NULL");
   if ((uintptr_t)cu->data % (uintptr_t)element_size(cu->dtype))
@@ -284,7 +288,9 @@ int ssm_sizes(const gdn_tensor* x, const gdn_tensor* b, const gdn_tensor* cu, co
     P->cut = P->segs_per_seq > 1;
     P->max_segs = P->segs_per_seq * P->seq.n;
   }
-  if (P->max_segs >= kMax32 || P->max_segs * P->H >= kMax32 - 8)
+  // a launch has fewer than 2^32 threads (the scan's: 4 P per segment and
+  // head, its segments rounded up by up to 7)
+  if ((P->max_segs + 7) * P->H * 4 * P->P >= kMaxThreads || (P->cut && P->seq.n * P->H * 256 >= kMaxThreads))
     return api_fail(GDN_ERR_SHAPE, "too many (segment, head) pairs");
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -352,7 +358,7 @@ int gdn_short_conv(const gdn_tensor* x, const gdn_tensor* weight, const float* b
   const int64_t D = x->shape[x->ndim - 1], W = weight->shape[1];
   if (weight->shape[0] != D) return api_fail(GDN_ERR_SHAPE, "weight must be [D, W]");
   if (W < 1 || W > 4) return api_fail(GDN_ERR_SHAPE, "W must be 1 .. 4 (got %lld)", (long long)W);
-  if (D < 1 || D >= kMax32) return api_fail(GDN_ERR_SHAPE, "D must be 1 .. 2^31 - 1");
+  if (D < 1 || D > kMaxCount) return api_fail(GDN_ERR_SHAPE, "D must be 1 .. 2^31 - 2^21");
   if (!contiguous(weight)) return api_fail(GDN_ERR_LAYOUT, "weight must be contiguous");
   if ((uintptr_t)bias % 4) return api_fail(GDN_ERR_LAYOUT, "bias must be 4-byte aligned");
   Sequences seq;
@@ -565,7 +571,7 @@ int gdn_ssm_decode(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor* 
   if (!head_dim(P.N) || !head_dim(P.P)) return api_fail(GDN_ERR_UNSUPPORTED, "N and P must be 16, 32, 64 or 128");
   if (P.H < 1 || P.G < 1 || P.H % P.G) return api_fail(GDN_ERR_SHAPE, "heads must be a positive multiple of groups");
   if (P.H > 65535) return api_fail(GDN_ERR_UNSUPPORTED, "at most 65535 heads");
-  if (n >= kMax32 || n * P.H * 8 >= kMax32) return api_fail(GDN_ERR_SHAPE, "too many (sequence, head) pairs");
+  if (n > kMaxCount) return api_fail(GDN_ERR_SHAPE, "too many sequences");
   if ((rc = check_state(state, "state", n, P))) return rc;
   gdn::api_clear_error();
   if (n == 0) return GDN_OK;

@@ -13,21 +13,40 @@
 //
 // Precision.  In each product one operand is an input as stored (exact); the
 // other is fp32 and is fed as the sum of bf16 terms: two for the outputs (M
-// and S; 2^-17 of a product, below the output's own rounding), three for the
-// state (w_t x_t; 2^-25, so the fp32 state keeps fp32 accuracy).  The extra
-// matrix instructions stay under the time the block's bytes take.  fp32
-// inputs use fp32 matrix instructions throughout.
+// and S; 2^-16 of a product, below the output's own rounding), three for the
+// state where it is handed on (w_t x_t; 2^-24, so the fp32 state keeps fp32
+// accuracy) and two where only this segment's outputs read it.  fp32 inputs
+// use fp32 matrix instructions throughout.  Sums of steps are run in fp64.
 //
-// A workgroup scans one segment of one head, the state in the accumulators
-// of its waves (each wave holds all N rows of its CW columns).  The fragment
-// layout along the contraction index is the accumulators' own (k-tile order,
-// gdn_device.h), so the state and x feed the products without leaving their
-// lanes; b and c are stored in LDS with that order inside each row, x in its
-// own order and read transposed.
+// A workgroup of eight waves scans one segment of one 128-column head or of
+// two 64-column ones (fewer waves for fewer columns), in blocks of C = 32
+// tokens, the state in the accumulators of its waves (each wave holds all N
+// rows of 16 columns).  The fragment layout along the contraction index is
+// the accumulators' own, so the state and x feed the products without leaving
+// their lanes; b, c and x lie in LDS as in memory (granules swizzled), and
+// what meets the token axis is read transposed.  All waves copy the tiles of
+// the coming blocks straight to LDS, b and c two blocks ahead (the next
+// block's M is formed beside this block's products, so that a block needs one
+// barrier), x one.
 //
 // A sequence cut into segments takes three launches: the segments' end
 // states from zero (the same kernel without c and y), their joining in
 // order, and the scan of all segments at once.
+//
+// What bounds it: not the bytes (16384 tokens x 48 heads of 128 x 128 in
+// bf16: 546 MB in 291 us, 1.9 TB/s) nor LDS (44 % busy; tiles laid out with
+// half the bank conflicts took as long), but issue.  A wave issues about 243
+// vector instructions and 38 matrix ones a block, 96 of the former to split
+// the state into terms; a matrix instruction of 16 cycles lets two vector
+// instructions of other waves in where four would fit (both measured), so
+// the two together take about 75 % of a SIMD's cycles (counters: vector unit
+// 60 %, matrix cores 31 %), and the block's barrier the rest.  Measured on
+// that case: 16 columns a wave in blocks of 32 (128 registers, two
+// workgroups a compute unit), 305 us, against 496 for 32 columns in blocks of
+// 64 (one workgroup); two blocks a barrier for the segments' states and
+// batched joining, 291.  No faster: copies by a ninth wave, ageing the state
+// less often, raised priority for the matrix phases, deeper rings, the split
+// by dot products (they take the matrix unit's slots).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -76,14 +95,6 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// The same without a wait: for the copying wave, which waits for its copies
-// itself, and its partner before the first block.
-__device__ __forceinline__ void ssm_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
 }
 
 // First row of lane group q's four rows of state tile nt.  bf16 pairs the
@@ -737,7 +748,8 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
 // [previous end, T], so that a malformed table can only give wrong results.
 // One workgroup, a sequence per thread and round, the scans over waves by
 // shuffles; each thread writes its own sequence's rows, or, of a sequence of
-// many segments, all threads do.
+// many segments, all threads do.  Bound by its two trips to memory and four
+// barriers (3.8 us for 64 prompts).
 constexpr int kSsmTableThreads = 1024;
 
 __global__ __launch_bounds__(kSsmTableThreads) void ssm_table_kernel(SsmTable p) {
@@ -812,7 +824,9 @@ hipError_t launch_ssm_table(const SsmTable& p, hipStream_t s) {
 // Joins a sequence's segments: the state before segment s is its
 // predecessor's end state plus the predecessor's decay times the state before
 // that one; after the last, the final state.  A thread takes four elements of
-// a (sequence, head) state; `parts` workgroups share the vecs of one.
+// a (sequence, head) state; `parts` workgroups share the vecs of one.  The
+// order is a chain, so eight slots are asked for at once: bound by that trip
+// to memory (16 heads x 16 segments 6.7 us, 48 heads x 10 segments 10 us).
 constexpr int kSsmJoinThreads = 256;
 
 template <typename TI, int N, int P>
@@ -865,6 +879,10 @@ __global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, 
 // HBM.  A workgroup takes CB columns of one head's state; each thread holds
 // four adjacent columns of a band of rows, read and written with 16-byte
 // accesses; the contraction with c is reduced over the bands through LDS.
+// 32 columns a workgroup give enough of them to fill the chip from a few
+// sequences on; all of a thread's rows are asked for before the first is
+// used.  256 sequences x 16 heads of 128 x 128: 96 us, 5.6 TB/s (a large copy
+// reaches 4.8); one sequence x 48 heads: 4.4 us, the launch and two trips.
 
 template <int N, int P>
 struct SsmStepShape {
@@ -931,7 +949,7 @@ template <typename TI, int N, int P, int HP>
 static hipError_t launch_ssm_kernel(bool out, const SsmParams& p, hipStream_t s) {
   const int64_t units = (int64_t)p.max_segs * (p.heads / p.unit);
   const int64_t blocks = (units + 7) / 8 * 8 * (p.unit / HP);
-  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  if (blocks > kLaunchThreads / (SsmShape<TI, N, P, HP, true>::THREADS)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), threads(SsmShape<TI, N, P, HP, true>::THREADS);
   if (out)
     hipLaunchKernelGGL((ssm_kernel<TI, N, P, HP, true>), grid, threads, 0, s, p);
@@ -961,19 +979,32 @@ static hipError_t launch_ssm_np(bool out, const SsmParams& given, hipStream_t s)
   const int64_t units = (int64_t)p.n_seq * p.heads;
   const int all = (N * P / 4 + kSsmJoinThreads - 1) / kSsmJoinThreads;
   const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(all, 1024 / units));
-  if (units * parts >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+  if (units * parts > kLaunchThreads / kSsmJoinThreads) return hipErrorInvalidValue;
   hipLaunchKernelGGL((ssm_join_kernel<TI, N, P>), dim3((unsigned)(units * parts)), dim3(kSsmJoinThreads), 0, s, p,
                      parts);
   return hipGetLastError();
 }
 
 template <typename TI, int N, int P>
-static hipError_t launch_ssm_step_np(const SsmStepParams& p, hipStream_t s) {
+static hipError_t launch_ssm_step_np(const SsmStepParams& all, hipStream_t s) {
   using D = SsmStepShape<N, P>;
-  const int64_t blocks = (int64_t)p.n * p.heads * (P / D::CB);
-  if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((ssm_step_kernel<TI, N, P>), dim3((unsigned)blocks), dim3(D::NT), 0, s, p);
-  return hipGetLastError();
+  const int64_t each = (int64_t)all.heads * (P / D::CB);  // workgroups of a sequence
+  const int64_t most = kLaunchThreads / D::NT / each;     // sequences of a launch
+  if (most < 1) return hipErrorInvalidValue;
+  for (int64_t i = 0; i < all.n; i += most) {
+    SsmStepParams p = all;
+    p.n = (int)std::min<int64_t>(most, all.n - i);
+    p.x = (const TI*)all.x + i * all.x_st;
+    p.dt = all.dt + i * all.dt_st;
+    p.b = (const TI*)all.b + i * all.b_st;
+    p.c = (const TI*)all.c + i * all.c_st;
+    p.state = all.state + i * all.heads * N * P;
+    p.out = (TI*)all.out + i * all.o_st;
+    hipLaunchKernelGGL((ssm_step_kernel<TI, N, P>), dim3((unsigned)(p.n * each)), dim3(D::NT), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 #define GDN_SSM_SIZES(X) \

@@ -479,8 +479,9 @@ int gdn_check_cu_seqlens(const int32_t* cu_host, int64_t n_seq, int64_t t_total)
  * validation on the host before any HIP call, work enqueued on the caller's
  * stream, nothing allocated, no synchronisation.  An output may share memory
  * with an input only where its description says so; other overlaps are
- * GDN_ERR_LAYOUT.  All sums, norms and states are fp32, and each output is
- * rounded once.
+ * GDN_ERR_LAYOUT, and so are output rows that overlap each other (a token or
+ * head stride of zero).  All sums, norms and states are fp32, and each output
+ * is rounded once.  Tokens, sequences and channels: at most 2^31 - 2^21.
  */
 
 /*
@@ -523,8 +524,9 @@ int gdn_short_conv(const gdn_tensor* x, const gdn_tensor* weight, const float* b
  * the delta rule's (d_k x d_v, here N x P), so both mixers' states can share
  * one pool.  d_t >= 0 is a precondition without GDN_SSM_SOFTPLUS.  Inputs
  * are expected to be finite: a NaN or infinity reaches the later tokens of
- * its own sequence and may reach up to 63 earlier ones; it never reaches
- * another sequence or head.
+ * its own sequence and may reach up to 31 earlier ones (its block of the
+ * matrix products); one in x or dt stays in its head, one in b or c in its
+ * group's heads, and none reaches another sequence.
  */
 #define GDN_SSM_SOFTPLUS 1u
 typedef struct gdn_ssm_options {
@@ -554,8 +556,11 @@ void gdn_ssm_default_options(gdn_ssm_options* opts);
  *   workspace   gdn_ssm_workspace_size() bytes of device memory, 256-byte
  *               aligned (NULL if that is 0); not to be used by another call
  *               that overlaps on the device
- * Sizes: N, P in {16, 32, 64, 128}; T < 2^31; layout of x, b, c and out as
- * gdn_prefill's (16-byte vector accesses, else GDN_ERR_LAYOUT).
+ * Sizes: N, P in {16, 32, 64, 128}; at most 65535 heads; (segments + 7) x
+ * heads x 4 P < 2^32, and sequences x heads < 2^24 where sequences are cut
+ * (GDN_ERR_SHAPE).  Layout of x, b, c and out as gdn_prefill's (16-byte
+ * vector accesses), token strides at most 2^24 elements, else GDN_ERR_LAYOUT;
+ * dt's strides are any (token stride at most 2^24).
  */
 int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor* b,
                     const gdn_tensor* c, const gdn_tensor* cu_seqlens,

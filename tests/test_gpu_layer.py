@@ -283,3 +283,22 @@ def test_norm_past_two_gib():
     out, *_ = G.gdn_add_rms_norm(x, out=torch.empty_like(x), out_q=q, scales=s)
     check_norm(dict(x=x[-2:], residual=None, weight=None), {"out": out[-2:], "out_q": q[-2:], "scales": s[-2:]}, 128,
                "norm far rows")
+
+
+@pytest.mark.parametrize("dtype,group", [(BF16, 0), (F32, 128)])
+def test_norm_more_rows_than_one_launch(dtype, group):
+    """Rows around 2^21, where the library starts another launch."""
+    R, D, at = (1 << 21) + 7, 40, 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(3)
+    big = torch.empty(R, 48, dtype=dtype, device="cuda").normal_(generator=g)
+    x, res = big[:, :D], torch.empty(R, D, dtype=dtype, device="cuda").normal_(generator=g)
+    w = torch.rand(D, generator=g, device="cuda")
+    q = torch.zeros(R, D, dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.zeros((R, 1) if group else (R,), device="cuda")
+    out, ro, *_ = G.gdn_add_rms_norm(x, res, w, residual_out=torch.zeros_like(res), out=torch.zeros_like(res),
+                                     out_q=q, scales=s)
+    for rows in (slice(0, 5), slice(at - 5, at + 5), slice(R - 3, R)):
+        check_norm(dict(x=x[rows], residual=res[rows], weight=w),
+                   {"out": out[rows], "residual_out": ro[rows], "out_q": q[rows], "scales": s[rows]}, group,
+                   f"rows {rows.start}")
+    assert (s > 0).all() and (out.float().abs().sum(1) > 0).all()

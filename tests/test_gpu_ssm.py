@@ -278,3 +278,20 @@ def test_step_state_past_two_gib():
     (y, s), (my, ms) = reference(d1, [1])
     U.check(out[-1:], y, U.HALF[BF16] * np.abs(y) + U.STEP_F32 * my, "far step")
     U.check(state[-1:], s, U.STEP_F32 * ms, "far step state")
+
+
+def test_step_of_more_sequences_than_one_launch():
+    """2^32 threads and more: 64 of each 16 x 16 state (64 GiB of states)."""
+    n, N = (1 << 26) + 5, 16
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, b, c = (torch.empty(n, 1, N, dtype=BF16, device="cuda").normal_(generator=g) for _ in range(3))
+    dt = torch.rand(n, 1, generator=g, device="cuda")
+    state = torch.zeros(n, 1, N, N, device="cuda")
+    out = G.gdn_ssm_decode(x, dt, b, c, state, softplus=False)
+    for rows in (slice(0, 3), slice((1 << 26) - 4, n)):
+        d = dict(x=x[rows], dt=dt[rows], b=b[rows], c=c[rows], a_log=None, dt_bias=None, d_skip=None, init=None)
+        k = rows.stop - rows.start
+        (y, s), (my, ms) = reference(d, [1] * k, act=False)
+        U.check(out[rows], y, U.HALF[BF16] * np.abs(y) + U.STEP_F32 * my, "step")
+        U.check(state[rows], s, U.STEP_F32 * ms, "state")
+    assert (out.float().abs().sum((1, 2)) > 0).float().mean() > 0.999

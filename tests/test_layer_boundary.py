@@ -247,6 +247,27 @@ def test_norm_refusals(lib):
 # the header and the binding
 
 
+def test_counts_at_the_limits(lib):
+    """Counts that a kernel's 32-bit counters could run past are refused."""
+    most = (1 << 31) - (1 << 21)
+    at = dict(bias=None, x=fake((most + 1, 8)), out=fake((most + 1, 8), addr=1 << 44))
+    expect(conv(lib, D=8, **at), SHAPE)
+    assert "2^31 - 2^21" in message()
+    expect(conv(lib, x=fake((1, most + 1)), out=fake((1, most + 1)), w=fake((most + 1, 4), F32, addr=1 << 44)), SHAPE)
+    expect(conv(lib, cu=fake((most + 2,), I32)), SHAPE)
+    n = ctypes.c_size_t(0)
+    # launches of 2^32 threads: 4 P per segment and head in the scan, 256 per
+    # sequence and head where segments are joined
+    cut = opts(segment_blocks=1)
+    for T, H, P, n_seq, o, want in [
+            (most + 1, 1, 16, None, None, SHAPE), (most, 1, 16, None, None, 0), (100, 1, 16, most + 1, None, SHAPE),
+            (4096, 4000, 64, 4180, None, 0), (4096, 4000, 64, 4190, None, SHAPE),
+            (4096, 4000, 16, 4190, cut, 0), (4096, 4000, 16, 4195, cut, SHAPE), (4096, 4000, 16, 4195, None, 0)]:
+        x, b = fake((T, H, P)), fake((T, 1, 16))
+        cu = None if n_seq is None else fake((n_seq + 1,), I32)
+        expect(lib.gdn_ssm_workspace_size(ref(x), ref(b), ref(cu), ref(o), ctypes.byref(n)), want)
+
+
 def test_options_struct_matches_the_header(tmp_path):
     src = tmp_path / "l.c"
     src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "gdn.h"\nint main(void) {\n'
