@@ -302,7 +302,7 @@ hipError_t launch_short_conv(bool bf16, bool vec, const ShortConvParams& p, hipS
 // run on registers.  Rows of up to 1024 columns take one wave each, longer
 // ones a workgroup.  Measured: 4096 rows of 5120 columns in bf16 with residual
 // and both outputs 44 us, 4.3 TB/s; 131071 rows of 6144 with 8-bit output
-// alone 994 us, 5.7 TB/s; eight rows 3.9 us, the launch, one trip and the
+// alone 932 us, 6.1 TB/s; eight rows 3.9 us, the launch, one trip and the
 // reductions.
 
 constexpr int kNormVec = 8;
@@ -315,17 +315,32 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
 }
 
+// 16-byte accesses, past the caches where FAR.
+typedef unsigned norm_u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned norm_u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename V, bool FAR>
+__device__ __forceinline__ V norm_ld(const void* p) {
+  return FAR ? __builtin_nontemporal_load((const V*)p) : *(const V*)p;
+}
+
+template <bool FAR, typename V>
+__device__ __forceinline__ void norm_st(void* p, V v) {
+  if constexpr (FAR) __builtin_nontemporal_store(v, (V*)p);
+  else *(V*)p = v;
+}
+
 // Eight columns from c0 on, those at or after d as zeros.
-template <typename TI, bool VEC>
+template <typename TI, bool VEC, bool FAR = false>
 __device__ __forceinline__ void norm_load(float (&v)[kNormVec], const TI* row, int c0, int d) {
   if constexpr (VEC) {
     if constexpr (sizeof(TI) == 2) {
-      const uint4 r = ld16(row + c0);
+      const norm_u32x4 r = norm_ld<norm_u32x4, FAR>(row + c0);
       const TI* e = (const TI*)&r;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
     } else {
-      const f32x4 a = *(const f32x4*)(row + c0), b = *(const f32x4*)(row + c0 + 4);
+      const f32x4 a = norm_ld<f32x4, FAR>(row + c0), b = norm_ld<f32x4, FAR>(row + c0 + 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = a[i];
@@ -338,15 +353,15 @@ __device__ __forceinline__ void norm_load(float (&v)[kNormVec], const TI* row, i
   }
 }
 
-template <typename TI, bool VEC>
+template <typename TI, bool VEC, bool FAR>
 __device__ __forceinline__ void norm_store(TI* row, const float (&v)[kNormVec], int c0, int d) {
   if constexpr (VEC) {
     if constexpr (sizeof(TI) == 2) {
-      uint4 r;
+      norm_u32x4 r;
       TI* e = (TI*)&r;
 #pragma unroll
       for (int i = 0; i < 8; ++i) e[i] = from_float<TI>(v[i]);
-      st16(row + c0, r);
+      norm_st<FAR>(row + c0, r);
     } else {
       f32x4 a, b;
 #pragma unroll
@@ -354,8 +369,8 @@ __device__ __forceinline__ void norm_store(TI* row, const float (&v)[kNormVec], 
         a[i] = v[i];
         b[i] = v[4 + i];
       }
-      *(f32x4*)(row + c0) = a;
-      *(f32x4*)(row + c0 + 4) = b;
+      norm_st<FAR>(row + c0, a);
+      norm_st<FAR>(row + c0 + 4, b);
     }
   } else {
 #pragma unroll
@@ -367,7 +382,7 @@ __device__ __forceinline__ void norm_store(TI* row, const float (&v)[kNormVec], 
 // Eight columns times inv as e4m3 (the hardware conversion rounds to nearest
 // even; |v inv| is at most 448 up to fp32 rounding, and everything below 464
 // rounds into the range).
-template <bool VEC>
+template <bool VEC, bool FAR>
 __device__ __forceinline__ void norm_store_q(uint8_t* row, const float (&v)[kNormVec], float inv, int c0,
                                              int d) {
   int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
@@ -375,7 +390,7 @@ __device__ __forceinline__ void norm_store_q(uint8_t* row, const float (&v)[kNor
   int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
   b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, b, true);
   if constexpr (VEC) {
-    *(uint2*)(row + c0) = make_uint2((unsigned)a, (unsigned)b);
+    norm_st<FAR>(row + c0, (norm_u32x2){(unsigned)a, (unsigned)b});
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -399,7 +414,7 @@ __device__ __forceinline__ float row_reduce(float v, float* lds, F f) {
   return v;
 }
 
-template <typename TI, int TPR, int NV, bool VEC>
+template <typename TI, int TPR, int NV, bool VEC, bool FAR>
 __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(NormParams p) {
   constexpr int RPB = TPR > 64 ? 1 : 4;  // rows per workgroup
   __shared__ float s_sum[16], s_max[16];
@@ -416,10 +431,10 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(Norm
 #pragma unroll
     for (int e = 0; e < kNormVec; ++e) v[i][e] = 0.f;
     if (c0 < p.d) {
-      norm_load<TI, VEC>(v[i], x, c0, p.d);
+      norm_load<TI, VEC, FAR>(v[i], x, c0, p.d);
       if (res) {
         float r[kNormVec];
-        norm_load<TI, VEC>(r, res, c0, p.d);
+        norm_load<TI, VEC, FAR>(r, res, c0, p.d);
 #pragma unroll
         for (int e = 0; e < kNormVec; ++e) v[i][e] += r[e];
       }
@@ -428,7 +443,7 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(Norm
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c0 = (sub + i * TPR) * kNormVec;
-    if (p.res_out && c0 < p.d) norm_store<TI, VEC>((TI*)p.res_out + row * p.ro_st, v[i], c0, p.d);
+    if (p.res_out && c0 < p.d) norm_store<TI, VEC, FAR>((TI*)p.res_out + row * p.ro_st, v[i], c0, p.d);
 #pragma unroll
     for (int e = 0; e < kNormVec; ++e) ss += v[i][e] * v[i][e];
   }
@@ -453,7 +468,7 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(Norm
         v[i][e] = v[i][e] * rn * w[e];
         if (VEC || c0 + e < p.d) top = max_nan(top, fabsf(v[i][e]));
       }
-      if (p.out) norm_store<TI, VEC>((TI*)p.out + row * p.o_st, v[i], c0, p.d);
+      if (p.out) norm_store<TI, VEC, FAR>((TI*)p.out + row * p.o_st, v[i], c0, p.d);
     }
     if (p.out_q && p.groups) {
       // a group's 128 columns are 16 adjacent lanes, all of them here (those
@@ -462,7 +477,7 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(Norm
       for (int off = 1; off < 16; off <<= 1) top = max_nan(top, __shfl_xor(top, off));
       const float scale = max_nan(top, kScaleFloor) / kE4m3Max;
       if (live) {
-        norm_store_q<VEC>(p.out_q + row * p.q_st, v[i], 1.f / scale, c0, p.d);
+        norm_store_q<VEC, FAR>(p.out_q + row * p.q_st, v[i], 1.f / scale, c0, p.d);
         if ((sub & 15) == 0) p.scales[row * p.groups + c0 / 128] = scale;
       }
     }
@@ -476,19 +491,19 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(Norm
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c0 = (sub + i * TPR) * kNormVec;
-      if (c0 < p.d) norm_store_q<VEC>(p.out_q + row * p.q_st, v[i], inv, c0, p.d);
+      if (c0 < p.d) norm_store_q<VEC, FAR>(p.out_q + row * p.q_st, v[i], inv, c0, p.d);
     }
   }
 }
 
-template <typename TI, bool VEC>
+template <typename TI, bool VEC, bool FAR>
 static hipError_t launch_add_rms_norm_t(const NormParams& p, hipStream_t s) {
   const int vecs = (p.d + kNormVec - 1) / kNormVec;
   const bool wave = vecs <= 128;
   const int64_t blocks = wave ? (p.rows + 3) / 4 : p.rows;
 #define GDN_NORM(TPR, NV)                                                                             \
   do {                                                                                                \
-    hipLaunchKernelGGL((add_rms_norm_kernel<TI, TPR, NV, VEC>), dim3((unsigned)blocks),                \
+    hipLaunchKernelGGL((add_rms_norm_kernel<TI, TPR, NV, VEC, FAR>), dim3((unsigned)blocks),                \
                        dim3(TPR > 64 ? TPR : 256), 0, s, p);                                          \
     return hipGetLastError();                                                                         \
   } while (0)
@@ -505,8 +520,21 @@ static hipError_t launch_add_rms_norm_t(const NormParams& p, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
+template <typename TI>
+static hipError_t launch_add_rms_norm_v(bool vec, bool far, const NormParams& p, hipStream_t s) {
+  if (!vec) return launch_add_rms_norm_t<TI, false, false>(p, s);
+  return far ? launch_add_rms_norm_t<TI, true, true>(p, s) : launch_add_rms_norm_t<TI, true, false>(p, s);
+}
+
 hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& all, hipStream_t s) {
   const int64_t size = bf16 ? 2 : 4;
+  // What the memory-side cache (256 MiB) cannot hold between this operator
+  // and its neighbours goes past the caches: 131071 rows of 6144 (5.7 GB)
+  // 994 -> 942 us, 16384 of 5120 with their neighbours 226 -> 209; below, the
+  // neighbours lose what this operator gains (4096 rows 34 -> 30 us alone,
+  // 59 -> 61 with them; 256 rows 6.4 -> 7.2).
+  const int64_t bytes = all.rows * all.d * (size * (1 + !!all.res + !!all.res_out + !!all.out) + !!all.out_q);
+  const bool far = bytes > (int64_t)256 << 20;
   constexpr int64_t most = (int64_t)1 << 21;  // rows of a launch, a row taking at most 1024 threads
   for (int64_t row = 0; row < all.rows; row += most) {
     NormParams p = all;
@@ -518,9 +546,7 @@ hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& all, hipSt
     p.out = at(all.out, all.o_st * size);
     p.out_q = at(all.out_q, all.q_st);
     p.scales = at(all.scales, (all.groups ? all.groups : 1) * 4);
-    const hipError_t e =
-        bf16 ? (vec ? launch_add_rms_norm_t<gdn::bf16, true>(p, s) : launch_add_rms_norm_t<gdn::bf16, false>(p, s))
-             : (vec ? launch_add_rms_norm_t<float, true>(p, s) : launch_add_rms_norm_t<float, false>(p, s));
+    const hipError_t e = bf16 ? launch_add_rms_norm_v<gdn::bf16>(vec, far, p, s) : launch_add_rms_norm_v<float>(vec, far, p, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

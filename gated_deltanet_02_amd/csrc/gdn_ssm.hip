@@ -879,15 +879,19 @@ __global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, 
 // HBM.  A workgroup takes CB columns of one head's state; each thread holds
 // four adjacent columns of a band of rows, read and written with 16-byte
 // accesses; the contraction with c is reduced over the bands through LDS.
-// 32 columns a workgroup give enough of them to fill the chip from a few
-// sequences on; all of a thread's rows are asked for before the first is
-// used.  256 sequences x 16 heads of 128 x 128: 96 us, 5.6 TB/s (a large copy
-// reaches 4.8); one sequence x 48 heads: 4.4 us, the launch and two trips.
+// All of a thread's rows are asked for before the first is used, and the
+// state, which nothing reads before the next token, goes past the caches
+// (nontemporal: 256 sequences x 16 heads of 128 x 128 in 96 -> 90 us, 6.0 TB/s
+// where a large copy reaches 4.8; 16 sequences 10.7 -> 8.2 us).  A workgroup
+// takes 16 KiB of state, N by 4096 / N columns: at 512 x 16 heads of 64 x 128
+// 92 us in 64 columns, 108 in 32, 99 in 128; of 32 x 128 46 us in 128 and 88
+// in 32; of 128 x 128 (256 sequences) 93 us in 32, 98 in 64.  One sequence x
+// 48 heads: 3.8 us, the launch and two trips.
 
 template <int N, int P>
 struct SsmStepShape {
-  static constexpr int CB = P < 32 ? P : 32;          // columns per workgroup
-  static constexpr int CG = CB / 4;                   // column groups
+  static constexpr int CB = P < 4096 / N ? P : 4096 / N;  // columns per workgroup
+  static constexpr int CG = CB / 4;                       // column groups
   static constexpr int RG = N < 256 / CG ? N : 256 / CG;  // row groups
   static constexpr int NT = CG * RG;
   static constexpr int RPT = N / RG;
@@ -906,7 +910,7 @@ __global__ __launch_bounds__((SsmStepShape<N, P>::NT)) void ssm_step_kernel(SsmS
   float* Hs = p.state + ((int64_t)u * N + r0) * P + c0;
   f32x4 hreg[RPT];
 #pragma unroll
-  for (int r = 0; r < RPT; ++r) hreg[r] = *(const f32x4*)(Hs + r * P);
+  for (int r = 0; r < RPT; ++r) hreg[r] = __builtin_nontemporal_load((const f32x4*)(Hs + r * P));
   const TI* br = (const TI*)p.b + (int64_t)i * p.b_st + (int64_t)grp * p.b_sh + r0;
   const TI* cr = (const TI*)p.c + (int64_t)i * p.c_st + (int64_t)grp * p.c_sh + r0;
   const f32x4 x = load4<TI>((const TI*)p.x + (int64_t)i * p.x_st + (int64_t)h * p.x_sh + c0);
@@ -923,7 +927,7 @@ __global__ __launch_bounds__((SsmStepShape<N, P>::NT)) void ssm_step_kernel(SsmS
       hn[e] = a * hreg[r][e] + bv * x[e];
       part[e] += cv * hn[e];
     }
-    *(f32x4*)(Hs + r * P) = hn;
+    __builtin_nontemporal_store(hn, (f32x4*)(Hs + r * P));
   }
   *(f32x4*)&sred[rg][4 * cg] = part;
   __syncthreads();
@@ -989,7 +993,7 @@ template <typename TI, int N, int P>
 static hipError_t launch_ssm_step_np(const SsmStepParams& all, hipStream_t s) {
   using D = SsmStepShape<N, P>;
   const int64_t each = (int64_t)all.heads * (P / D::CB);  // workgroups of a sequence
-  const int64_t most = kLaunchThreads / D::NT / each;     // sequences of a launch
+  const int64_t most = kLaunchThreads / D::NT / each;  // sequences of a launch
   if (most < 1) return hipErrorInvalidValue;
   for (int64_t i = 0; i < all.n; i += most) {
     SsmStepParams p = all;
