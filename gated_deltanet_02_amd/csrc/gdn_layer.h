@@ -64,6 +64,7 @@ struct SsmTable {
   int32_t* seg_off;
   int32_t* table;
   int32_t cu_i64, n_seq, t_total, seg_len, max_segs;
+  int32_t round;  // segments whose workgroups take a place in every compute unit
 };
 
 // gdn_ssm_decode.
@@ -101,8 +102,10 @@ hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& p, hipStre
 
 // Tokens per block of the scan: sequences are cut at multiples of it.
 constexpr int kSsmBlock = 64;
-// Workgroups the scan of a large problem is spread over.
+// Workgroups the scan of a large problem is spread over, and the heads that
+// one of them takes.
 int ssm_target_groups();
+int ssm_group_heads(bool bf16, int p, int group);
 hipError_t launch_ssm_table(const SsmTable& p, hipStream_t s);
 // The segments' end states and their joining (only when sequences are cut),
 // then the scan.

@@ -52,6 +52,21 @@ def test_scan_sizes(dtype, N, P):
     check_scan(d, out, fin, lengths, f"scan N={N} P={P} {dtype}")
 
 
+@pytest.mark.parametrize("n", [100, 128, 200, 256, 300, 512, 600])
+@pytest.mark.parametrize("P", [32, 64])
+def test_scan_many_sequences(n, P):
+    """Numbers of segments around those at which their order changes (two
+    heads, one or two workgroups a segment), lengths out of order, empty ones
+    among them, one long enough to be cut."""
+    lengths = [(37 * i * i + 11 * i) % 41 for i in range(n)]
+    lengths[n // 3] = 300
+    d = U.scan_inputs(n, sum(lengths), 2, 1, 32, P, BF16, n, init=True)
+    e = U.to_gpu(d)
+    for seg in (0, 1):
+        out, fin = run(e, lengths, segment_blocks=seg)
+        check_scan(d, out, fin, lengths, f"{n} sequences, segments {seg}")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("seg", [-1, 1, 2, 3])
 @pytest.mark.parametrize("init", [True, False])
