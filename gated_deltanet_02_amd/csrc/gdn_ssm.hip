@@ -34,7 +34,7 @@
 // order, and the scan of all segments at once.
 //
 // What bounds it: not the bytes (16384 tokens x 48 heads of 128 x 128 in
-// bf16: 546 MB in 291 us, 1.9 TB/s) nor LDS (44 % busy; tiles laid out with
+// bf16: 546 MB in 300 us, 1.8 TB/s) nor LDS (44 % busy; tiles laid out with
 // half the bank conflicts took as long), but issue.  A wave issues about 243
 // vector instructions and 38 matrix ones a block, 96 of the former to split
 // the state into terms; a matrix instruction of 16 cycles lets two vector
