@@ -100,7 +100,7 @@ struct NormParams {
 hipError_t launch_short_conv(bool bf16, bool vec, const ShortConvParams& p, hipStream_t s);
 hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& p, hipStream_t s);
 
-// Tokens per block of the scan: sequences are cut at multiples of it.
+// Segments are multiples of this many tokens (two of the scan's blocks).
 constexpr int kSsmBlock = 64;
 // Workgroups the scan of a large problem is spread over, and the heads that
 // one of them takes.
