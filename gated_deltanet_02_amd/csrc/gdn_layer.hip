@@ -61,6 +61,16 @@ __device__ __forceinline__ int conv_cu(const ShortConvParams& p, int i) {
   return (int)min(max(e, (int64_t)0), (int64_t)p.t_total);
 }
 
+// The last of the sequences lo .. hi that starts at or before token t (lo if
+// none does).
+__device__ __forceinline__ int conv_find(const ShortConvParams& p, int lo, int hi, int t) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (conv_cu(p, mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // What a thread loads of a row, and its values.
 template <typename TI, bool VEC>
 struct ConvRaw {
@@ -172,13 +182,8 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
     if (p.cu) {
       t0 = item * tile;
       t1 = min(t0 + tile, conv_cu(p, p.n_seq));
-      int lo = 0, hi = p.n_seq - 1;  // largest sequence starting at or before t0
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (conv_cu(p, mid) <= t0) lo = mid; else hi = mid - 1;
-      }
-      seq = lo;
       last = p.n_seq - 1;
+      seq = conv_find(p, 0, last, t0);
       start = conv_cu(p, seq);
       end = conv_cu(p, seq + 1);
     } else {
@@ -224,8 +229,9 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
 #pragma unroll
       for (int i = 0; i < kConvGroup; ++i) {
         if (t + i >= t1) break;
-        while (t + i >= end && seq < last) {
-          ++seq;
+        if (t + i >= end && seq < last) {
+          // the next sequence, or the one behind a run of empty ones
+          if (conv_cu(p, ++seq + 1) <= t + i) seq = conv_find(p, seq, last, t + i);
           start = conv_cu(p, seq);
           end = conv_cu(p, seq + 1);
         }

@@ -1,0 +1,49 @@
+"""The short convolution at counts past what a launch or a 32-bit sum of two
+indices holds (GPU)."""
+import time
+
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_02_amd as G
+from oracle import layer
+from tests import layer_util as U
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def far_apart(n, lengths, dtype, W=3):
+    """Sequences 0 .. n - 1 with the given lengths at some indices, the rest
+    empty, one channel, against float64."""
+    cu = torch.zeros(n + 1, dtype=dtype, device="cuda")
+    for i, length in lengths.items():
+        cu[i + 1:] += length
+    T = sum(lengths.values())
+    g = U.gen(1)
+    x, w, bias = U.randn(g, T, 1), U.randn(g, 1, W), U.randn(g, 1)
+    d = U.to_gpu(dict(x=x, w=w, bias=bias))
+    out = torch.full((T, 1), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    began = time.monotonic()
+    G.gdn_short_conv(d["x"], d["w"], d["bias"], cu_seqlens=cu, out=out)
+    torch.cuda.synchronize()
+    took = time.monotonic() - began
+    y, _, mag = layer.short_conv(U.f64(x), U.f64(w), U.f64(bias), [lengths[i] for i in sorted(lengths)])
+    U.check(out, y, U.HALF[F32] * np.abs(y) + U.CONV_F32 * (mag + 1), f"{n} sequences, {took:.3f} s")
+    return took
+
+
+def test_long_runs_of_empty_sequences():
+    """Are passed over, not walked through: 2^24 of them one by one are that
+    many loads in a row, some seconds."""
+    n = 1 << 24
+    assert far_apart(n, {0: 50, 2: 3, n // 2: 70, n // 2 + 1: 1, n - 1: 33}, torch.int32) < 1.0
