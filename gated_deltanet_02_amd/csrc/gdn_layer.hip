@@ -65,7 +65,7 @@ __device__ __forceinline__ int conv_cu(const ShortConvParams& p, int i) {
 // none does).
 __device__ __forceinline__ int conv_find(const ShortConvParams& p, int lo, int hi, int t) {
   while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
+    const int mid = lo + ((hi - lo + 1) >> 1);  // (lo + hi can pass 2^31)
     if (conv_cu(p, mid) <= t) lo = mid; else hi = mid - 1;
   }
   return lo;

@@ -47,3 +47,11 @@ def test_long_runs_of_empty_sequences():
     many loads in a row, some seconds."""
     n = 1 << 24
     assert far_apart(n, {0: 50, 2: 3, n // 2: 70, n // 2 + 1: 1, n - 1: 33}, torch.int32) < 1.0
+
+
+@pytest.mark.parametrize("cu_type", [torch.int32, torch.int64])
+def test_more_than_two_to_the_thirty_sequences(cu_type):
+    """Nearly all of them empty; those with tokens lie at both ends, so that
+    the search for a token's sequence adds indices whose sum passes 2^31."""
+    n = (1 << 30) + 9
+    far_apart(n, {0: 50, 2: 3, n - 9: 70, n - 3: 1, n - 1: 33}, cu_type)

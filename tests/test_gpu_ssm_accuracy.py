@@ -1,0 +1,84 @@
+"""How exact the state space scan is, token by token, beside 64 bits (GPU):
+fp32 inputs against bounds of their own, and decays of every size in both
+types.
+
+Bounds for fp32 inputs.  Everything is then formed in fp32, each rounding at
+most 2^-24.  A sum of n terms of like size and random sign rounds n times at
+the size of its partial sums: together sqrt(n / 2) 2^-24 of the result's size.
+An output passes through three such sums, c.b and S^T c over N <= 128 (8 each)
+and M x over 32 tokens (4), and a state through the 32 tokens of each block
+(4) and one more rounding a block (at most 6 for 64 blocks without decay); a
+step, its decay and their exponent carry about 4 roundings that a token's
+products share.  sqrt(8^2 + 8^2 + 4^2 + 4^2) < 13 and 13 2^-24 < 2^-20: the
+root mean square, over tokens and heads, of an output vector's relative
+error, and of a head's state likewise, stays below 2^-20 (one output in two
+bf16 terms would reach 2^-19).  No single vector is further off than 2^-19 of
+the same sums over absolute values.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_02_amd as G
+from oracle import layer
+from tests import layer_util as U
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def check_vectors(got, want, mag, axes, label):
+    """The two bounds above; a vector is what ``axes`` span."""
+    got = U.f64(got)
+    assert np.isfinite(got).all(), f"{label}: not finite"
+    norm = lambda v: np.sqrt((np.asarray(v) ** 2).sum(axes))  # noqa: E731
+    err, size, most = norm(got - want), norm(want), norm(mag)
+    rms = float(np.sqrt(np.mean((err / np.maximum(size, 1e-300)) ** 2)))
+    worst = float((err / np.maximum(most, 1e-300)).max())
+    print(f"  {label}: rms {rms:.2e}, worst {worst:.2e} of the absolute sums", flush=True)
+    assert rms <= 2.0 ** -20, label
+    assert worst <= 2.0 ** -19, label
+
+
+def check(d, lengths, label, **kw):
+    e = U.to_gpu(d)
+    fin = torch.empty(len(lengths), e["x"].shape[1], e["b"].shape[2], e["x"].shape[2], device="cuda")
+    out, _ = G.gdn_ssm_prefill(e["x"], e["dt"], e["b"], e["c"], e["a_log"], e["dt_bias"], e["d_skip"],
+                               U.cu_of(lengths).cuda(), e["init"], final_state=fin, **kw)
+    a = [U.f64(d[k]) for k in ("x", "dt", "b", "c", "a_log", "dt_bias", "d_skip")]
+    y, s = layer.ssm_scan(*a, lengths=lengths, init=U.f64(d["init"]))
+    my, ms = layer.ssm_magnitude(*a, lengths=lengths, init=U.f64(d["init"]))
+    if d["x"].dtype == F32:
+        check_vectors(out, y, my, 2, label + " out")
+        check_vectors(fin, s, ms, (2, 3), label + " state")
+    else:
+        U.check(out, y, U.HALF[BF16] * np.abs(y) + U.SCAN_OUT * my, label + " out")
+        U.check(fin, s, U.SCAN_STATE * ms, label + " state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rate", [1.0, 16.0, 148.0])
+@pytest.mark.parametrize("step", [2.0, 20.0, 100.0, 1000.0, 1e6])
+def test_large_steps_among_small_ones(dtype, rate, step):
+    """Single tokens whose step ends all memory, at every place of a tile of
+    16, among ordinary ones: what follows them is as exact as anything else.
+    Half of them carry nothing of their own, so that the tokens behind them
+    are seen."""
+    lengths = [16 * 17 + 5, 40]
+    T, H = sum(lengths), 2
+    d = U.scan_inputs(int(step) % 97 + int(rate), T, H, 1, 32, 64, dtype, 2, init=True)
+    d["a_log"] = torch.full((H,), rate).log()
+    d["dt_bias"] = torch.full((H,), -4.0)
+    at = torch.arange(0, T, 17)  # 0, 1, 2, ... of their tiles
+    d["dt"][at] = step + 4.0
+    d["dt"][at[::3] + 2] = step + 4.0  # a second one two tokens on
+    d["x"][at[::2]] = 0.0
+    for seg in (-1, 1):
+        check(d, lengths, f"rate {rate} step {step} {dtype} segments {seg}", segment_blocks=seg)
