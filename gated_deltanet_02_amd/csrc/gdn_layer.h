@@ -25,6 +25,7 @@ struct ShortConvParams {
   int32_t cu_i64;
   int32_t n_seq, seq_len;  // uniform: n_seq sequences of seq_len tokens
   int32_t t_total, d, width, silu;
+  int64_t first_item, end_item;  // a launch's work items (set by the launcher)
 };
 
 // The scan's problem sizes, and the rule that cuts sequences into segments.

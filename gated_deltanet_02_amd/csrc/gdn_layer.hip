@@ -99,16 +99,15 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
   // in order, so that neighbouring tiles share an L2
   const unsigned per = (gridDim.x + 7) / 8, id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   const int cb = id % blocks_c, tx = threadIdx.x % cols;
-  const int64_t item64 = (int64_t)(id / blocks_c) * (kConvThreads / cols) + threadIdx.x / cols;
+  const int64_t item64 = p.first_item + (int64_t)(id / blocks_c) * (kConvThreads / cols) + threadIdx.x / cols;
   const int first = cb * cols * E;  // the workgroup's first channel
   const int c0 = first + tx * E;
-  const bool live = item64 < (int64_t)n_tiles + p.n_seq && c0 < p.d;
-  const int item = live ? (int)item64 : 0;
+  const bool live = item64 < p.end_item && c0 < p.d;
   const TI* x = (const TI*)p.x + c0;
   TI* out = (TI*)p.out + c0;
   // What a sequence's own item reads, asked for before the taps are turned:
   // the history, the first rows, the last rows.
-  const int own = live ? item - n_tiles : -1;  // its sequence, or < 0: a tile
+  const int own = live && item64 >= n_tiles ? (int)(item64 - n_tiles) : -1;  // its sequence, or < 0: a tile
   int own_start = 0, own_len = 0;
   ConvRaw<TI, VEC> hist[W], head[W], tail[W];
   const TI* hin = nullptr;
@@ -176,7 +175,8 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
       for (int e = 0; e < E; ++e) rows[j][e] = rows[j + 1][e];
   };
 
-  if (item < n_tiles) {
+  if (own < 0) {
+    const int item = (int)item64;
     // tokens [t0, t1), the current sequence's start and end
     int t0, t1, start, end, seq = 0, last = 0;
     if (p.cu) {
@@ -280,9 +280,9 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
 }
 
 template <typename TI, bool VEC>
-static hipError_t launch_short_conv_t(const ShortConvParams& p, hipStream_t s) {
+static hipError_t launch_short_conv_t(const ShortConvParams& all, hipStream_t s) {
   constexpr int E = ConvVec<TI, VEC>::n;
-  const int64_t nvec = (p.d + E - 1) / E;
+  const int64_t nvec = (all.d + E - 1) / E;
   int cols = 1;
   while (cols < nvec && cols < kConvThreads) cols *= 2;
   const int64_t blocks_c = (nvec + cols - 1) / cols;
@@ -290,23 +290,34 @@ static hipError_t launch_short_conv_t(const ShortConvParams& p, hipStream_t s) {
   // than one workgroup each per SIMD (1237 rows of 1001 channels: 9.2 us in
   // tiles of 32, 6.1 us in tiles of 8)
   int tile = kConvTile;
-  while (tile > 2 * kConvGroup && (int64_t)p.t_total / tile * nvec < 1024 * kConvThreads) tile /= 2;
+  while (tile > 2 * kConvGroup && (int64_t)all.t_total / tile * nvec < 1024 * kConvThreads) tile /= 2;
   // sequences of fewer than W tokens have no tokens for the tiles
-  const int64_t per_seq = p.cu ? 0 : p.seq_len < p.width ? 0 : (p.seq_len + tile - 1) / tile;
-  const int64_t tiles = p.cu ? ((int64_t)p.t_total + tile - 1) / tile : per_seq * p.n_seq;
-  const int64_t items = tiles + p.n_seq, per_block = kConvThreads / cols;
-  const int64_t blocks = ((items + per_block - 1) / per_block * blocks_c + 7) / 8 * 8;
-  if (items >= ((int64_t)1 << 31) || blocks > kLaunchThreads / kConvThreads) return hipErrorInvalidValue;
-  switch (p.width) {
+  const int64_t per_seq = all.cu ? 0 : all.seq_len < all.width ? 0 : (all.seq_len + tile - 1) / tile;
+  const int64_t tiles = all.cu ? ((int64_t)all.t_total + tile - 1) / tile : per_seq * all.n_seq;
+  const int64_t items = tiles + all.n_seq, per_block = kConvThreads / cols;
+  // over as many launches as the items take (in any order: an item reads and
+  // writes no other's history)
+  const int64_t most = (kLaunchThreads / kConvThreads - 7) / blocks_c * per_block;
+  for (int64_t first = 0; first < items; first += most) {
+    ShortConvParams p = all;
+    p.first_item = first;
+    const int64_t n = items - first < most ? items - first : most;
+    p.end_item = first + n;
+    const int64_t blocks = ((n + per_block - 1) / per_block * blocks_c + 7) / 8 * 8;
+    switch (p.width) {
 #define GDN_CONV(W)                                                                                        \
-    case W:                                                                                                \
-      hipLaunchKernelGGL((short_conv_kernel<TI, W, VEC>), dim3((unsigned)blocks), dim3(kConvThreads), 0, s, p, \
-                         cols, (int)blocks_c, tile, (int)per_seq, (int)tiles);                                   \
-      return hipGetLastError();
-    GDN_CONV(1) GDN_CONV(2) GDN_CONV(3) GDN_CONV(4)
+      case W:                                                                                              \
+        hipLaunchKernelGGL((short_conv_kernel<TI, W, VEC>), dim3((unsigned)blocks), dim3(kConvThreads), 0, s, p, \
+                           cols, (int)blocks_c, tile, (int)per_seq, (int)tiles);                           \
+        break;
+      GDN_CONV(1) GDN_CONV(2) GDN_CONV(3) GDN_CONV(4)
 #undef GDN_CONV
+      default: return hipErrorInvalidValue;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  return hipErrorInvalidValue;
+  return hipSuccess;
 }
 
 hipError_t launch_short_conv(bool bf16, bool vec, const ShortConvParams& p, hipStream_t s) {

@@ -55,3 +55,25 @@ def test_more_than_two_to_the_thirty_sequences(cu_type):
     the search for a token's sequence adds indices whose sum passes 2^31."""
     n = (1 << 30) + 9
     far_apart(n, {0: 50, 2: 3, n - 9: 70, n - 3: 1, n - 1: 33}, cu_type)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_more_steps_than_one_launch(packed):
+    """2^24 workgroups and more: one token for each of 8.4 million sequences,
+    the histories in place, each read and written once."""
+    D, W, split = 257, 2, 8388604  # two workgroups a sequence
+    n = split + 50
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, state = (torch.empty(n, D, dtype=BF16, device="cuda").normal_(generator=g) for _ in range(2))
+    w, bias = torch.randn(D, W, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda")
+    rows = [slice(0, 4), slice(split // 2, split // 2 + 4), slice(split - 8, split + 8), slice(n - 4, n)]
+    before = [state[r].clone() for r in rows]
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda") if packed else None
+    out = torch.zeros(n, D, dtype=BF16, device="cuda")
+    G.gdn_short_conv(x if packed else x[:, None], w, bias, cu_seqlens=cu, state_in=state[:, None],
+                     state_out=state[:, None], out=out if packed else out[:, None])
+    assert torch.equal(state, x)
+    for r, old in zip(rows, before):
+        k = r.stop - r.start
+        y, _, mag = layer.short_conv(U.f64(x[r]), U.f64(w), U.f64(bias), [1] * k, U.f64(old[:, None]))
+        U.check(out[r], y, U.HALF[BF16] * np.abs(y) + U.CONV_F32 * (mag + 1), f"rows from {r.start}")
