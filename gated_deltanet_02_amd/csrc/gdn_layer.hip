@@ -413,16 +413,25 @@ __device__ __forceinline__ void norm_store(TI* row, const float (&v)[kNormVec], 
   }
 }
 
-// Eight columns times inv as e4m3 (the hardware conversion rounds to nearest
-// even; |v inv| is at most 448 up to fp32 rounding, and everything below 464
-// rounds into the range).
+// Eight columns over their scale as e4m3 (the hardware conversion rounds to
+// nearest even; |v / scale| is at most 448 up to fp32 rounding, and everything
+// below 464 rounds into the range).  The fp32 quotient is the rounded one:
+// v (1 / scale) corrected once by its remainder, without which codes next to
+// a tie would flip.  (Under an infinite scale nothing is left but v * 0.)
 template <bool VEC, bool FAR>
-__device__ __forceinline__ void norm_store_q(uint8_t* row, const float (&v)[kNormVec], float inv, int c0,
+__device__ __forceinline__ void norm_store_q(uint8_t* row, const float (&v)[kNormVec], float scale, int c0,
                                              int d) {
-  int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-  a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, a, true);
-  int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
-  b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, b, true);
+  const float inv = 1.f / scale, by = scale < __builtin_inff() ? scale : 0.f;
+  float u[kNormVec];
+#pragma unroll
+  for (int i = 0; i < kNormVec; ++i) {
+    const float q = v[i] * inv;
+    u[i] = __builtin_fmaf(-__builtin_fmaf(q, by, -v[i]), inv, q);  // (keeps the sign of a zero)
+  }
+  int a = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], 0, false);
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], a, true);
+  int b = __builtin_amdgcn_cvt_pk_fp8_f32(u[4], u[5], 0, false);
+  b = __builtin_amdgcn_cvt_pk_fp8_f32(u[6], u[7], b, true);
   if constexpr (VEC) {
     norm_st<FAR>(row + c0, (norm_u32x2){(unsigned)a, (unsigned)b});
   } else {
@@ -511,7 +520,7 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(Norm
       for (int off = 1; off < 16; off <<= 1) top = max_nan(top, __shfl_xor(top, off));
       const float scale = max_nan(top, kScaleFloor) / kE4m3Max;
       if (live) {
-        norm_store_q<VEC, FAR>(p.out_q + row * p.q_st, v[i], 1.f / scale, c0, p.d);
+        norm_store_q<VEC, FAR>(p.out_q + row * p.q_st, v[i], scale, c0, p.d);
         if ((sub & 15) == 0) p.scales[row * p.groups + c0 / 128] = scale;
       }
     }
@@ -520,12 +529,11 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(Norm
   if (p.out_q && !p.groups) {
     big = row_reduce<TPR>(big, s_max, [](float a, float b) { return max_nan(a, b); });
     const float scale = max_nan(big, kScaleFloor) / kE4m3Max;
-    const float inv = 1.f / scale;
     if (sub == 0) p.scales[row] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c0 = (sub + i * TPR) * kNormVec;
-      if (c0 < p.d) norm_store_q<VEC, FAR>(p.out_q + row * p.q_st, v[i], inv, c0, p.d);
+      if (c0 < p.d) norm_store_q<VEC, FAR>(p.out_q + row * p.q_st, v[i], scale, c0, p.d);
     }
   }
 }
