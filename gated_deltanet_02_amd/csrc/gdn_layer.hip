@@ -341,6 +341,7 @@ hipError_t launch_short_conv(bool bf16, bool vec, const ShortConvParams& p, hipS
 
 constexpr int kNormVec = 8;
 constexpr float kE4m3Max = 448.f;
+constexpr float kNormLeast = 0x1p-100f;   // mean squares from here on lose no digits to underflow
 constexpr float kScaleFloor = 0x1p-100f;  // keeps a scale and its reciprocal finite
 
 // The larger of two non-negative floats; a NaN (its bits are the larger
@@ -460,7 +461,7 @@ __device__ __forceinline__ float row_reduce(float v, float* lds, F f) {
 template <typename TI, int TPR, int NV, bool VEC, bool FAR>
 __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(NormParams p) {
   constexpr int RPB = TPR > 64 ? 1 : 4;  // rows per workgroup
-  __shared__ float s_sum[16], s_max[16];
+  __shared__ float s_sum[16], s_max[16], s_again[16];
   const int sub = TPR > 64 ? threadIdx.x : threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * RPB + (TPR > 64 ? 0 : threadIdx.x >> 6);
   if (row >= p.rows) return;
@@ -491,7 +492,23 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void add_rms_norm_kernel(Norm
     for (int e = 0; e < kNormVec; ++e) ss += v[i][e] * v[i][e];
   }
   ss = row_reduce<TPR>(ss, s_sum, [](float a, float b) { return a + b; });
-  const float rn = 1.f / sqrtf(ss / (float)p.d + p.eps);
+  float eps = p.eps, mean = ss / (float)p.d;
+  if (!(mean + eps >= kNormLeast && mean < __builtin_inff())) {
+    // squares past fp32's range (or NaN, or real infinities, which give the
+    // same again): once more, of the row times a power of two
+    const float by = mean < 1.f ? 0x1p100f : 0x1p-76f;
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < kNormVec; ++e) {
+        v[i][e] *= by;
+        ss += v[i][e] * v[i][e];
+      }
+    mean = row_reduce<TPR>(ss, s_again, [](float a, float b) { return a + b; }) / (float)p.d;
+    eps = eps * by * by;
+  }
+  const float rn = 1.f / sqrtf(mean + eps);
   float big = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
