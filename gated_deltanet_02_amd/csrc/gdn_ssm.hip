@@ -72,13 +72,14 @@ struct SsmShape {
   static constexpr bool HALF = TPU == 2 && NT % 2 == 1;  // N = 16: half a unit
   static constexpr int TU = RT / TPU;               // units along the tokens
   static constexpr int TILES = RT * (RT + 1) / 2;   // of M
-  // LDS: rings of b (and c), of x, of the blocks' decays, and M's two buffers
-  static constexpr int BB = C * N * S, XB = C * P * S, MB = 3072, WB = 4 * C * 4;
-  static constexpr int RB = OUT ? 3 : 4, RX = OUT ? 2 : 4, RW = 4;
+  // LDS: rings of b (and c), of x, of the blocks' weights (and, for M, which
+  // is a block ahead, of its sums and steps), and M's two buffers
+  static constexpr int BB = C * N * S, XB = C * P * S, MB = 3072, WB = 2 * C * 4, GB = OUT ? 2 * C * 4 + C * 2 : 0;
+  static constexpr int RB = OUT ? 3 : 4, RX = OUT ? 2 : 4, RW = 4, RG = RB;
   static constexpr int bc = BB * (OUT ? 2 : 1);     // b, then c
   // (each head has its own x, M and decays)
   static constexpr int o_x = RB * bc, o_m = o_x + HP * RX * XB, o_w = o_m + (OUT ? HP * 2 * MB : 0);
-  static constexpr int total = o_w + HP * RW * WB;
+  static constexpr int o_g = o_w + HP * RW * WB, total = o_g + HP * RG * GB;
 };
 
 // Granule g of a row sits at granule g ^ swizzle: the four rows of a lane
@@ -295,7 +296,7 @@ struct SsmCopy {
       const uint32_t o = (uint32_t)row * (uint32_t)stride + (uint32_t)((g % GR) ^ ssm_swz<GR>(row)) * 16u;
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                    :
-                   : "s"(tile + piece * 1024), "v"(o), "s"(words)
+                   : "s"(__builtin_amdgcn_readfirstlane(tile + piece * 1024)), "v"(o), "s"(words)
                    : "memory", "m0");
     }
   }
@@ -412,13 +413,19 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
   const float rate = -expf(p.a_log ? p.a_log[h] : 0.f) * kLog2e;
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
   // Steps d and decays of blocks blk and blk + 1 (tokens past the end have
-  // step 0).  In logarithms to base 2, with the sum run in fp64 (an fp32 sum
-  // of, say, -100 would leave 4e-6 in the difference of two neighbours):
+  // step 0).  In logarithms to base 2:
   //   c  sum of the token's own tile of 16 up to it,   E = 2^c,
   //   f  d 2^(the tile's sum - c)
-  auto weigh = [&](int blk, float raw) {
+  // The sum is run in fp64, and M, which needs its differences, gets it as a
+  // float and its remainder: one large step leaves a sum of, say, -1000 for
+  // the rest of the tile, of which a float alone would leave 3e-5 in the
+  // difference of two neighbours.  A decay past 2^-160 is zero in fp32 and so
+  // is every sum that it is part of; held there, sums end at -2560, with
+  // remainders below 2^-13, which 2^12 brings into the fp16 range.
+  auto weigh = [&](int blk, float raw, int g0, int g1) {
     const float d = blk * C + lane < sg.n ? ssm_step_size(bias, raw, p.softplus) : 0.f;
     double c = (double)rate * (double)d;
+    c = c < -160. ? -160. : c;
 #pragma unroll
     for (int off = 1; off < 16; off <<= 1) {
       const double o = __shfl_up(c, off, 16);
@@ -426,17 +433,27 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     }
     const double end = __shfl(c, 15, 16);
     float* w = (float*)(smem + D::o_w + (((blk + (lane >> 5)) & (D::RW - 1)) * HP + hh) * D::WB) + (lane & 31);
-    w[0] = (float)c;
-    w[C] = d;
-    w[2 * C] = d * __builtin_amdgcn_exp2f((float)(end - c));
-    w[3 * C] = __builtin_amdgcn_exp2f((float)c);
+    w[0] = d * __builtin_amdgcn_exp2f((float)(end - c));
+    w[C] = __builtin_amdgcn_exp2f((float)c);
+    if constexpr (OUT) {
+      char* g = smem + D::o_g + (g0 * HP + hh) * D::GB + (lane >> 5) * ((g1 - g0) * HP * D::GB);
+      float* s = (float*)g + (lane & 31);
+      s[0] = (float)c;
+      s[C] = d;
+      ((_Float16*)(g + 8 * C))[lane & 31] = (_Float16)((float)(c - (double)(float)c) * 0x1p12f);
+    }
   };
   copy_bc(0, 0);
   copy_bc(1, 1);
   copy_x(0, 0);
   if constexpr (!OUT) copy_x(1, 1);
-  // pairs of blocks are weighed by the waves in turn
-  float raw = fetch_steps(2 * wh);
+  // Pairs of blocks are weighed in turn by the waves of the SIMD that has the
+  // least of M to form (the fourth one's none of its three tiles; 64 prompts x
+  // 16 heads of 64 columns: 327 us, 341 with all waves in turn), without M by
+  // all waves.
+  constexpr int LAST = OUT ? std::min(NH, 4) - 1 : 0, WN = NH / (LAST + 1);
+  const int turn = (wh & LAST) == LAST ? wh >> (LAST == 3 ? 2 : LAST) : -1;
+  float raw = turn >= 0 ? fetch_steps(2 * turn) : 0.f;
 
   // The state before the segment.  Tile (nt, ct), lane (q, m), element e:
   // row ssm_state_row(nt, q) + e, column col0 + 16 ct + m.
@@ -489,7 +506,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
   // [16 jt + 4 q + e], an operand's layout; one tile (0,0), (1,0), (1,1) a wave.
   // bf16: the two terms of tile (0,0) as half units at 0 and 1536, of (1, jt)
   // as the halves of full units at 512 and 2048; fp32: a unit per tile.
-  auto form_m = [&](const char* sB, const float* w, char* sM) {
+  auto form_m = [&](const char* sB, const float* w, const char* g, char* sM) {
     const int q = l8 >> 7, m = (l8 >> 3) & 15;
 #pragma unroll 1
     for (int tile = wh; tile < D::TILES; tile += NH) {
@@ -499,18 +516,23 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
       for (int u = 0; u < NU; ++u) mma_unit<HALF>(acc, rows.unit(sB, jt, u), rows.unit(sB + D::BB, it, u));
       f32x4 v;
       if (it == jt) {
-        const f32x4 cj = *(const f32x4*)(w + 16 * jt + 4 * q), dj = *(const f32x4*)(w + C + 16 * jt + 4 * q);
-        const float ci = w[16 * it + m];
+        typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+        const float* s = (const float*)g;
+        const _Float16* rest = (const _Float16*)(g + 8 * C);
+        const f32x4 cj = *(const f32x4*)(s + 16 * jt + 4 * q), dj = *(const f32x4*)(s + C + 16 * jt + 4 * q);
+        const f16x4 rj = *(const f16x4*)(rest + 16 * jt + 4 * q);
+        const float ci = s[16 * it + m], ri = (float)rest[16 * it + m] * 0x1p-12f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = 4 * q + e;
-          v[e] = acc[e] * (__builtin_amdgcn_exp2f(j <= m ? ci - cj[e] : -__builtin_inff()) * dj[e]) +
+          const float diff = (ci - cj[e]) + __builtin_fmaf((float)rj[e], -0x1p-12f, ri);
+          v[e] = acc[e] * (__builtin_amdgcn_exp2f(j <= m ? diff : -__builtin_inff()) * dj[e]) +
                  (j == m ? skip : 0.f);
         }
       } else {
         // through the end of column tile 0, which lies between j and i
-        const f32x4 fj = *(const f32x4*)(w + 2 * C + 4 * q);
-        const float ei = w[3 * C + 16 + m];
+        const f32x4 fj = *(const f32x4*)(w + 4 * q);
+        const float ei = w[C + 16 + m];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = acc[e] * fj[e] * ei;
       }
@@ -528,15 +550,15 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     }
   };
 
-  if (wh == 0) {
-    weigh(0, raw);
-    raw = fetch_steps(2 * NH);
+  if (turn == 0) {
+    weigh(0, raw, 0, 1);
+    raw = fetch_steps(2 * WN);
   }
   int rb = 0, rx = 0;
   __builtin_amdgcn_s_waitcnt(ssm_vmcnt(0));  // (the copies, the raw steps)
   if constexpr (OUT) {
     lds_barrier();
-    form_m(smem, (const float*)(smem + D::o_w + hh * D::WB), smem + D::o_m + hh * D::MB);
+    form_m(smem, (const float*)(smem + D::o_w + hh * D::WB), smem + D::o_g + hh * D::GB, smem + D::o_m + hh * D::MB);
   }
   for (int t = 0; t < blocks; ++t) {
     if constexpr (OUT) {
@@ -554,9 +576,9 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
       copy_bc(t + 3, rb ^ 3);
       copy_x(t + 3, rx ^ 3);
     }
-    if ((t & 1) == 0 && ((t >> 1) + 1) % NH == wh) {
-      weigh(t + 2, raw);
-      raw = fetch_steps(t + 2 + 2 * NH);
+    if ((t & 1) == 0 && ((t >> 1) + 1) % WN == turn) {
+      weigh(t + 2, raw, rb == 0 ? 2 : rb - 1, rb);  // (a turn back is two on in a ring of three)
+      raw = fetch_steps(t + 2 + 2 * WN);
     }
     // the places in the tiles, kept as they are: addresses derived from them
     // outside the loop would take more registers than there are
@@ -567,7 +589,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     const float* w = (const float*)(smem + D::o_w + ((t & (D::RW - 1)) * HP + hh) * D::WB);
     rb = rb + 1 == D::RB ? 0 : rb + 1;
     rx = rx + 1 == D::RX ? 0 : rx + 1;
-    const float e0 = w[3 * C + 15], e1 = w[3 * C + 31];
+    const float e0 = w[C + 15], e1 = w[C + 31];
     const float alpha = e0 * e1;
     decay *= alpha;
     U xu[TU][CT];  // this wave's columns of x
@@ -604,7 +626,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
       }
 #pragma unroll
       for (int it = 0; it < RT; ++it) {
-        const float e = it == 0 ? w[3 * C + m] : w[3 * C + 16 + m] * e0;
+        const float e = it == 0 ? w[C + m] : w[C + 16 + m] * e0;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -643,7 +665,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
       }
       // the next block's M
       form_m(smem + rb * D::bc, (const float*)(smem + D::o_w + (((t + 1) & (D::RW - 1)) * HP + hh) * D::WB),
-             smem + D::o_m + (((t + 1) & 1) * HP + hh) * D::MB);
+             smem + D::o_g + (rb * HP + hh) * D::GB, smem + D::o_m + (((t + 1) & 1) * HP + hh) * D::MB);
     }
 
     if constexpr (OUT) {
@@ -667,10 +689,10 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
 #pragma unroll
       for (int tu = 0; tu < TU; ++tu) {
         // w = d 2^(the block's sum - the sum up to the token)
-        f32x4 w0 = *(const f32x4*)(w + 2 * C + 16 * TPU * tu + 4 * q);
+        f32x4 w0 = *(const f32x4*)(w + 16 * TPU * tu + 4 * q);
         if (tu == 0) w0 *= e1;
         if constexpr (S == 2) {
-          const f32x4 w1 = *(const f32x4*)(w + 2 * C + 16 + 4 * q);
+          const f32x4 w1 = *(const f32x4*)(w + 16 + 4 * q);
           bf16x8 a[TERMS][CT];
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {

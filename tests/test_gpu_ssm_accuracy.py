@@ -14,6 +14,19 @@ root mean square, over tokens and heads, of an output vector's relative
 error, and of a head's state likewise, stays below 2^-20 (one output in two
 bf16 terms would reach 2^-19).  No single vector is further off than 2^-19 of
 the same sums over absolute values.
+
+A decay e^-x from an exponent that is rounded (d, the rate and their product:
+four roundings) is x 4 2^-24 off.  Steps up to 1 keep x e^-x below 0.4 and add
+nothing to the above; what a step of s leaves behind is still of the size of
+the rest where it has decayed by 1 / s, and adds ln(s) 2^-22 to both bounds.
+
+Two sizes that a relative error cannot be taken of.  fp32 ends at 2^-126, so a
+memory decayed by e^-300 has to come out as 0: vectors below 2^-100 count as
+of that size.  And behind a token whose step d ends all memory, out = (D +
+d c.b) x is one number times x: where that number nearly vanishes, its terms
+still round at their own sizes.  N = 32 products of random sign come to
+0.28 of their absolute sum in the root mean square (sqrt(32) against 32
+(2 / pi)) and to less than 1/16 of it in one of six; those count as 1/16.
 """
 import numpy as np
 import pytest
@@ -34,20 +47,22 @@ def _gpu():
         pytest.skip("no GPU")
 
 
-def check_vectors(got, want, mag, axes, label):
-    """The two bounds above; a vector is what ``axes`` span."""
+def check_vectors(got, want, mag, axes, label, step):
+    """The two bounds above; a vector is what ``axes`` span, ``step`` the largest
+    step."""
+    more = np.log(max(step, 1.0)) * 2.0 ** -22
     got = U.f64(got)
     assert np.isfinite(got).all(), f"{label}: not finite"
     norm = lambda v: np.sqrt((np.asarray(v) ** 2).sum(axes))  # noqa: E731
     err, size, most = norm(got - want), norm(want), norm(mag)
-    rms = float(np.sqrt(np.mean((err / np.maximum(size, 1e-300)) ** 2)))
-    worst = float((err / np.maximum(most, 1e-300)).max())
+    rms = float(np.sqrt(np.mean((err / np.maximum(np.maximum(size, most / 16), 2.0 ** -100)) ** 2)))
+    worst = float((err / np.maximum(most, 2.0 ** -100)).max())
     print(f"  {label}: rms {rms:.2e}, worst {worst:.2e} of the absolute sums", flush=True)
-    assert rms <= 2.0 ** -20, label
-    assert worst <= 2.0 ** -19, label
+    assert rms <= 2.0 ** -20 + more, label
+    assert worst <= 2.0 ** -19 + more, label
 
 
-def check(d, lengths, label, **kw):
+def check(d, lengths, label, step=1.0, **kw):
     e = U.to_gpu(d)
     fin = torch.empty(len(lengths), e["x"].shape[1], e["b"].shape[2], e["x"].shape[2], device="cuda")
     out, _ = G.gdn_ssm_prefill(e["x"], e["dt"], e["b"], e["c"], e["a_log"], e["dt_bias"], e["d_skip"],
@@ -56,16 +71,16 @@ def check(d, lengths, label, **kw):
     y, s = layer.ssm_scan(*a, lengths=lengths, init=U.f64(d["init"]))
     my, ms = layer.ssm_magnitude(*a, lengths=lengths, init=U.f64(d["init"]))
     if d["x"].dtype == F32:
-        check_vectors(out, y, my, 2, label + " out")
-        check_vectors(fin, s, ms, (2, 3), label + " state")
+        check_vectors(out, y, my, 2, label + " out", step)
+        check_vectors(fin, s, ms, (2, 3), label + " state", step)
     else:
-        U.check(out, y, U.HALF[BF16] * np.abs(y) + U.SCAN_OUT * my, label + " out")
-        U.check(fin, s, U.SCAN_STATE * ms, label + " state")
+        U.check(out, y, U.HALF[BF16] * np.abs(y) + U.SCAN_OUT * my + 2.0 ** -100, label + " out")
+        U.check(fin, s, U.SCAN_STATE * ms + 2.0 ** -100, label + " state")
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rate", [1.0, 16.0, 148.0])
-@pytest.mark.parametrize("step", [2.0, 20.0, 100.0, 1000.0, 1e6])
+@pytest.mark.parametrize("step", [2.0, 20.0, 100.0, 1000.0, 1e6, 1e30])
 def test_large_steps_among_small_ones(dtype, rate, step):
     """Single tokens whose step ends all memory, at every place of a tile of
     16, among ordinary ones: what follows them is as exact as anything else.
@@ -81,4 +96,4 @@ def test_large_steps_among_small_ones(dtype, rate, step):
     d["dt"][at[::3] + 2] = step + 4.0  # a second one two tokens on
     d["x"][at[::2]] = 0.0
     for seg in (-1, 1):
-        check(d, lengths, f"rate {rate} step {step} {dtype} segments {seg}", segment_blocks=seg)
+        check(d, lengths, f"rate {rate} step {step} {dtype} segments {seg}", step, segment_blocks=seg)
