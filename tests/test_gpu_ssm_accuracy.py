@@ -97,3 +97,36 @@ def test_large_steps_among_small_ones(dtype, rate, step):
     d["x"][at[::2]] = 0.0
     for seg in (-1, 1):
         check(d, lengths, f"rate {rate} step {step} {dtype} segments {seg}", step, segment_blocks=seg)
+
+
+@pytest.mark.parametrize("N", [16, 32, 64, 128])
+@pytest.mark.parametrize("P", [16, 32, 64, 128])
+def test_fp32_sizes(N, P):
+    """Every head size, ragged lengths around the blocks, one cut."""
+    lengths = [1, 63, 64, 65, 0, 130, 2]
+    d = U.scan_inputs(N + 3 * P, sum(lengths), 4, 2, N, P, F32, len(lengths), init=True)
+    for seg in (-1, 1):
+        check(d, lengths, f"N={N} P={P} segments {seg}", segment_blocks=seg)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", ["none", "strong", "mixed", "zero", "large"])
+@pytest.mark.parametrize("rate", [1.0, 16.0, 148.0])
+def test_decay_ranges_and_rates(dtype, kind, rate):
+    """No memory lost, lost within a token, now and then, with steps of zero
+    and of some hundred, at every rate."""
+    lengths = [200, 64, 3]
+    d = U.scan_inputs(3, sum(lengths), 2, 1, 64, 64, dtype, 3, init=True)
+    d["a_log"] = torch.full((2,), -40.0) if kind == "none" else torch.full((2,), rate).log()
+    step = 1.0
+    if kind == "strong":
+        d["dt_bias"], step = torch.full((2,), 3.0), 8.0
+    elif kind == "mixed":
+        d["dt"] = torch.where(torch.rand(d["dt"].shape, generator=U.gen(9)) < 0.3, torch.tensor(12.0), d["dt"])
+        step = 12.0
+    elif kind == "zero":
+        d["dt"] = torch.full_like(d["dt"], -200.0)
+    elif kind == "large":
+        d["dt"], step = 100 + 100 * d["dt"].abs(), 600.0
+    for seg in (-1, 1):
+        check(d, lengths, f"{kind} rate {rate} {dtype} segments {seg}", step, segment_blocks=seg)
