@@ -243,6 +243,13 @@ __device__ __forceinline__ float ssm_step_size(float bias, float dt, int softplu
   return x > 20.f ? x : log1pf(expf(x));
 }
 
+// -scale e^a_log, held above minus infinity, so that a step of zero still
+// keeps all memory.
+__device__ __forceinline__ float ssm_rate(const float* a_log, int h, float scale) {
+  const float r = -expf(a_log ? a_log[h] : 0.f) * scale;
+  return r < -0x1.fffffep127f ? -0x1.fffffep127f : r;
+}
+
 typedef unsigned int ssm_u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int ssm_u32x4 __attribute__((ext_vector_type(4)));
 
@@ -410,7 +417,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     const __amdgpu_buffer_rsrc_t r = ssm_rows(pd + t * d_st, d_st, min(sg.n - t, 2 * C), 4);
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)((uint32_t)lane * (uint32_t)d_st), 0, 0));
   };
-  const float rate = -expf(p.a_log ? p.a_log[h] : 0.f) * kLog2e;
+  const float rate = ssm_rate(p.a_log, h, kLog2e);
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
   // Steps d and decays of blocks blk and blk + 1 (tokens past the end have
   // step 0).  In logarithms to base 2:
@@ -963,7 +970,7 @@ __global__ __launch_bounds__((SsmStepShape<N, P>::NT)) void ssm_step_kernel(SsmS
   const f32x4 x = load4<TI>((const TI*)p.x + (int64_t)i * p.x_st + (int64_t)h * p.x_sh + c0);
   const float d = ssm_step_size(p.dt_bias ? p.dt_bias[h] : 0.f, p.dt[(int64_t)i * p.dt_st + (int64_t)h * p.dt_sh],
                                 p.softplus);
-  const float a = expf(-expf(p.a_log ? p.a_log[h] : 0.f) * d);
+  const float a = expf(ssm_rate(p.a_log, h, 1.f) * d);
   f32x4 part = zero4();
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {

@@ -130,3 +130,25 @@ def test_decay_ranges_and_rates(dtype, kind, rate):
         d["dt"], step = 100 + 100 * d["dt"].abs(), 600.0
     for seg in (-1, 1):
         check(d, lengths, f"{kind} rate {rate} {dtype} segments {seg}", step, segment_blocks=seg)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rates_past_the_largest_float(dtype):
+    """e^a_log beyond fp32: any step ends all memory, a step of zero none; in
+    the scan and in the step."""
+    lengths, H = [45, 20], 2
+    d = U.scan_inputs(7, sum(lengths), H, 1, 32, 32, dtype, 2, init=True)
+    d["a_log"] = torch.tensor([100.0, 88.6])
+    d["dt"][::3] = -200.0
+    for seg in (-1, 1):
+        check(d, lengths, f"rates past the largest {dtype} segments {seg}", segment_blocks=seg)
+    d = U.scan_inputs(8, 6, H, 1, 32, 32, F32, 6, init=True)
+    d["a_log"] = torch.tensor([100.0, 88.6])
+    d["dt"][::2] = -200.0
+    e = U.to_gpu(d)
+    out = G.gdn_ssm_decode(e["x"], e["dt"], e["b"], e["c"], e["init"], e["a_log"], e["dt_bias"], e["d_skip"])
+    a = [U.f64(d[k]) for k in ("x", "dt", "b", "c", "a_log", "dt_bias", "d_skip")]
+    y, s = layer.ssm_scan(*a, lengths=[1] * 6, init=U.f64(d["init"]))
+    my, ms = layer.ssm_magnitude(*a, lengths=[1] * 6, init=U.f64(d["init"]))
+    check_vectors(out, y, my, 2, "step out", 1.0)
+    check_vectors(e["init"], s, ms, (2, 3), "step state", 1.0)
