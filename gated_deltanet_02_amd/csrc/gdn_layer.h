@@ -46,17 +46,24 @@ struct SsmParams {
   int32_t softplus;
   // segments: n_seq sequences; uniform ones have seq_len tokens and
   // segs_per_seq segments of seg_len tokens (the last may be shorter), packed
-  // ones are read from the table (sequence, first token, length) with
+  // ones are read from the table (sequence, first token, length, -1 or 4 times
+  // the slot plus 1 for a first segment, 2 for a last one) with
   // seg_off[n_seq + 1] giving each sequence's first segment
   int32_t packed, n_seq, seq_len, seg_len, segs_per_seq, max_segs;
   const int32_t* table;
   const int32_t* seg_off;
-  // per segment and head: the state before the segment (fragment order, see
-  // gdn_ssm.hip) and the segment's whole decay, and per sequence and head the
-  // last segment's end state; null when no sequence is cut
+  // Where sequences are cut (else null).  A sequence of two or more segments
+  // has a slot for each and one more: per slot and head the state before the
+  // segment (fragment order, see gdn_ssm.hip), in the last one the last
+  // segment's end state, and per slot and head the segment's whole decay.
+  // Uniform sequences have segs_per_seq + 1 slots each; of packed ones, cuts
+  // is (cut sequences, their segments, 0, 0) and then, for each, (sequence,
+  // first slot, segments, 0), and cut_table their segments' rows.
   float* slots;
   float* seg_decay;
-  float* ends;
+  const int32_t* cuts;
+  const int32_t* cut_table;
+  int32_t max_cuts, max_cut_segs;
 };
 
 // The segment table of a packed batch (see SsmParams).
@@ -64,7 +71,9 @@ struct SsmTable {
   const void* cu;   // [n_seq + 1] int32 or int64 (cu_i64)
   int32_t* seg_off;
   int32_t* table;
-  int32_t cu_i64, n_seq, t_total, seg_len, max_segs;
+  int32_t* cuts;  // this and the next: null when no sequence is cut
+  int32_t* cut_table;
+  int32_t cu_i64, n_seq, t_total, seg_len, max_segs, max_cuts, max_cut_segs;
   int32_t round;  // segments whose workgroups take a place in every compute unit
 };
 

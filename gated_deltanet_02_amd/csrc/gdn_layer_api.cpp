@@ -200,7 +200,8 @@ struct Ssm {
   gdn_ssm_options opts;
   int64_t seg_len = 0, segs_per_seq = 1, max_segs = 1;
   bool cut = false;  // some sequence may have two or more segments
-  size_t table = 0, seg_off = 0, slots = 0, ends = 0, decay = 0, total = 0;
+  int64_t max_cuts = 0, max_cut_segs = 0;  // such sequences, their segments
+  size_t table = 0, seg_off = 0, cuts = 0, cut_table = 0, slots = 0, decay = 0, total = 0;
 };
 
 int ssm_options(const gdn_ssm_options* opts, gdn_ssm_options* o) {
@@ -295,10 +296,16 @@ int ssm_sizes(const gdn_tensor* x, const gdn_tensor* b, const gdn_tensor* cu, co
     P->cut = P->T > P->seg_len;
     P->max_segs = P->T / P->seg_len + P->seq.n;
     P->segs_per_seq = 0;
+    // a cut sequence has at least seg_len + 1 tokens, and of its segments all
+    // but one are full
+    P->max_cuts = std::min<int64_t>(P->seq.n, P->T / (P->seg_len + 1));
+    P->max_cut_segs = P->T / P->seg_len + P->max_cuts;
   } else {
     P->segs_per_seq = std::max<int64_t>(1, (P->seq.len + P->seg_len - 1) / P->seg_len);
     P->cut = P->segs_per_seq > 1;
     P->max_segs = P->segs_per_seq * P->seq.n;
+    P->max_cuts = P->seq.n;
+    P->max_cut_segs = P->max_segs;
   }
   // a launch has fewer than 2^32 threads (the scan's: 4 P per segment and
   // head, its segments rounded up by up to 7)
@@ -315,9 +322,13 @@ int ssm_sizes(const gdn_tensor* x, const gdn_tensor* b, const gdn_tensor* cu, co
     P->seg_off = take((size_t)(P->seq.n + 1) * 4);
   }
   if (P->cut) {
-    P->decay = take((size_t)P->max_segs * P->H * 4);
-    P->slots = take((size_t)P->max_segs * P->H * P->N * P->P * 4);
-    P->ends = take((size_t)P->seq.n * P->H * P->N * P->P * 4);
+    if (P->seq.packed) {
+      P->cuts = take((size_t)(P->max_cuts + 1) * 16);
+      P->cut_table = take((size_t)P->max_cut_segs * 16);
+    }
+    const size_t slots = (size_t)(P->max_cut_segs + P->max_cuts);
+    P->decay = take(slots * P->H * 4);
+    P->slots = take(slots * P->H * P->N * P->P * 4);
   }
   P->total = off;
   return GDN_OK;
@@ -528,6 +539,8 @@ int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor*
   p.seg_len = (int32_t)P.seg_len;
   p.segs_per_seq = (int32_t)P.segs_per_seq;
   p.max_segs = (int32_t)P.max_segs;
+  p.max_cuts = (int32_t)P.max_cuts;
+  p.max_cut_segs = (int32_t)P.max_cut_segs;
   if (P.seq.packed) {
     p.table = (const int32_t*)(base + P.table);
     p.seg_off = (const int32_t*)(base + P.seg_off);
@@ -540,6 +553,12 @@ int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor*
     tp.t_total = (int32_t)P.T;
     tp.seg_len = (int32_t)P.seg_len;
     tp.max_segs = (int32_t)P.max_segs;
+    if (P.cut) {
+      tp.cuts = (int32_t*)(base + P.cuts);
+      tp.cut_table = (int32_t*)(base + P.cut_table);
+      tp.max_cuts = (int32_t)P.max_cuts;
+      tp.max_cut_segs = (int32_t)P.max_cut_segs;
+    }
     tp.round = (int32_t)(gdn::ssm_target_groups() / 2 / ssm_groups_per_segment(P));
     if ((e = gdn::launch_ssm_table(tp, s)) != hipSuccess)
       return api_fail(GDN_ERR_HIP, "segment table launch: %s", hipGetErrorString(e));
@@ -547,7 +566,8 @@ int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor*
   if (P.cut) {
     p.slots = (float*)(base + P.slots);
     p.seg_decay = (float*)(base + P.decay);
-    p.ends = (float*)(base + P.ends);
+    p.cuts = (const int32_t*)(base + P.cuts);
+    p.cut_table = (const int32_t*)(base + P.cut_table);
     if ((e = gdn::launch_ssm_states(P.bf16, (int)P.N, (int)P.P, p, s)) != hipSuccess)
       return api_fail(GDN_ERR_HIP, "segment states launch: %s", hipGetErrorString(e));
   }

@@ -311,24 +311,25 @@ struct SsmCopy {
 
 // Where a workgroup's segment lies.
 struct SsmSegment {
-  int seq, t0, n, slot;
+  int seq, t0, n, slot;  // slot < 0: the sequence is not cut
   bool first, last;  // of its sequence
 };
 
+template <bool OUT>
 __device__ __forceinline__ SsmSegment ssm_segment(const SsmParams& p, int s) {
   SsmSegment g;
   if (p.packed) {
-    const int4 row = *(const int4*)(p.table + 4 * (int64_t)s);
+    const int4 row = *(const int4*)((OUT ? p.table : p.cut_table) + 4 * (int64_t)s);
     g.seq = row.x;
     g.t0 = row.y;
     g.n = row.z;
-    g.slot = row.w;
-    g.first = g.slot == p.seg_off[g.seq];
-    g.last = g.slot + 1 == p.seg_off[g.seq + 1];
+    g.slot = row.w >> 2;
+    g.first = row.w & 1;
+    g.last = row.w & 2;
   } else {
-    g.slot = s;
     g.seq = s / p.segs_per_seq;
     const int j = s - g.seq * p.segs_per_seq;
+    g.slot = p.segs_per_seq > 1 ? s + g.seq : -1;
     g.t0 = g.seq * p.seq_len + j * p.seg_len;
     g.n = min(p.seg_len, p.seq_len - j * p.seg_len);
     g.first = j == 0;
@@ -374,11 +375,12 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
   const int h = item.head + hh;
   const int64_t state_elems = (int64_t)N * P;
 
-  if (p.packed && si >= p.seg_off[p.n_seq]) {
+  if (!OUT && p.packed && si >= p.cuts[1]) return;  // past the last cut segment
+  if (OUT && p.packed && si >= p.seg_off[p.n_seq]) {
     // past the last segment: empty sequences have none, and their state is
     // carried over here (there are at least as many such items as empty
     // sequences)
-    if (!OUT || !p.final_state) return;
+    if (!p.final_state) return;
     const int total = p.seg_off[p.n_seq];
     for (int i = si - total; i < p.n_seq; i += p.max_segs - total) {
       if (p.seg_off[i] != p.seg_off[i + 1]) continue;
@@ -387,10 +389,9 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
     }
     return;
   }
-  const SsmSegment sg = ssm_segment(p, si);
-  // sequences of one segment need no state from here, and a last segment's
-  // end state only as the final state
-  if (!OUT && sg.last && (sg.first || !p.final_state)) return;
+  const SsmSegment sg = ssm_segment<OUT>(p, si);
+  // a last segment's end state is needed only for the final state
+  if (!OUT && sg.last && !p.final_state) return;
   const int blocks = (sg.n + C - 1) / C;
   // The copies: each turn asks for what the next turn needs (b and c two
   // blocks ahead, since the next block's M is formed a block ahead; x one).
@@ -467,9 +468,9 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
   const int col0 = wh * D::CW;
   f32x4 H[NT][CT];
   const int64_t so = ((int64_t)sg.seq * p.heads + h) * state_elems;
-  float* slot = p.slots ? p.slots + ((int64_t)sg.slot * p.heads + h) * state_elems : nullptr;
+  float* slot = sg.slot >= 0 ? p.slots + ((int64_t)sg.slot * p.heads + h) * state_elems : nullptr;
   const int fr = wh * NT * CT * 256 + lane * 4;  // a wave's fragments in a slot
-  const bool from_slot = OUT && slot && !(sg.first && sg.last) && !(sg.first && !p.init);
+  const bool from_slot = OUT && slot && !(sg.first && !p.init);
   const float* from = sg.first && !from_slot ? p.init : nullptr;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -763,8 +764,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
             p.final_state[so + (int64_t)(ssm_state_row<TI, N>(nt, q) + e) * P + col0 + 16 * ct + m] = H[nt][ct][e];
     }
   } else {
-    // into the next segment's slot, or the sequence's end
-    float* dst = sg.last ? p.ends + so : slot + (int64_t)p.heads * state_elems;
+    float* dst = slot + (int64_t)p.heads * state_elems;  // the next slot
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -792,11 +792,15 @@ constexpr int kSsmTableThreads = 1024;
 constexpr int kSsmSort = 512;
 
 __global__ __launch_bounds__(kSsmTableThreads) void ssm_table_kernel(SsmTable p) {
-  __shared__ int s_end[16], s_sum[16], s_long[kSsmTableThreads][4], s_longs;
+  __shared__ int s_end[16], s_cut[16], s_long[kSsmTableThreads][6], s_longs;
+  __shared__ int64_t s_sum[16];
   __shared__ int4 s_row[kSsmSort];
   const bool sort = p.max_segs <= kSsmSort;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int carry_end = 0, carry = 0;  // of the rounds before
+  // of the rounds before: the end, the segments with the slots above them, the
+  // cut sequences
+  int carry_end = 0, carry_cut = 0;
+  int64_t carry = 0;
   if (tid == 0) p.seg_off[0] = 0;
   for (int base = 0; base < p.n_seq; base += kSsmTableThreads) {
     const int i = base + tid;
@@ -817,48 +821,70 @@ __global__ __launch_bounds__(kSsmTableThreads) void ssm_table_kernel(SsmTable p)
     const int start = max(lane > 0 ? prev : 0, before);
     end = max(end, before);
     const int n = i < p.n_seq ? (end - start + p.seg_len - 1) / p.seg_len : 0;
-    int sum = n;
+    const bool cut = n > 1;
+    const int64_t own = n + ((int64_t)(cut ? n + 1 : 0) << 32);
+    const uint64_t cuts = __ballot(cut);
+    int64_t sum = own;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(sum, off);
+      const int64_t o = __shfl_up(sum, off);
       if (lane >= off) sum += o;
     }
-    if (lane == 63) s_sum[wave] = sum;
+    if (lane == 63) {
+      s_sum[wave] = sum;
+      s_cut[wave] = __popcll(cuts);
+    }
     __syncthreads();
-    int first = carry;
-    for (int k = 0; k < 16; ++k) {
+    int64_t at = carry + sum - own;
+    int nth = carry_cut + __popcll(cuts & ((1ull << lane) - 1));  // of the cut sequences
+    const int waves = min((p.n_seq - base + 63) / 64, 16);  // the others add nothing
+#pragma unroll 4
+    for (int k = 0; k < waves; ++k) {
       carry_end = max(carry_end, s_end[k]);
       carry += s_sum[k];
-      if (k < wave) first += s_sum[k];
+      carry_cut += s_cut[k];
+      if (k < wave) {
+        at += s_sum[k];
+        nth += s_cut[k];
+      }
     }
-    first += sum - n;
+    const int first = (int)(uint32_t)at, slot = cut ? (int)(at >> 32) : -1;
     if (i < p.n_seq) p.seg_off[i + 1] = first + n;
-    auto row = [&](int seg, int seq, int from, int to, int k) {
+    if (cut && p.cuts && nth < p.max_cuts) *(int4*)(p.cuts + 4 * ((int64_t)nth + 1)) = make_int4(i, slot, n, 0);
+    // segment k of a sequence: its row, and that of a cut one once more
+    auto row = [&](int seg, int seq, int from, int to, int k, int slot, int row0) {
       if (seg >= p.max_segs) return;
-      const int t0 = from + k * p.seg_len;
-      const int4 r = make_int4(seq, t0, min(p.seg_len, to - t0), seg);
+      const int t0 = from + k * p.seg_len, n = min(p.seg_len, to - t0);
+      const int4 r = make_int4(seq, t0, n, slot < 0 ? -1 : 4 * (slot + k) + (k == 0 ? 1 : 0) + (t0 + n == to ? 2 : 0));
       if (sort) s_row[seg] = r;
       else *(int4*)(p.table + 4 * (int64_t)seg) = r;
+      if (slot >= 0 && p.cuts && row0 + k < p.max_cut_segs) *(int4*)(p.cut_table + 4 * (int64_t)(row0 + k)) = r;
     };
     if (n <= 4) {
-      for (int k = 0; k < n; ++k) row(first + k, i, start, end, k);
+      for (int k = 0; k < n; ++k) row(first + k, i, start, end, k, slot, slot - nth);
     } else {
-      const int at = atomicAdd(&s_longs, 1);  // (the order does not matter)
-      s_long[at][0] = first;
-      s_long[at][1] = i;
-      s_long[at][2] = start;
-      s_long[at][3] = end;
+      const int l = atomicAdd(&s_longs, 1);  // (the order does not matter)
+      s_long[l][0] = first;
+      s_long[l][1] = i;
+      s_long[l][2] = start;
+      s_long[l][3] = end;
+      s_long[l][4] = slot;
+      s_long[l][5] = slot - nth;
     }
     __syncthreads();
     for (int l = 0; l < s_longs; ++l) {
       const int from = s_long[l][2], to = s_long[l][3];
       for (int k = tid; k < (to - from + p.seg_len - 1) / p.seg_len; k += kSsmTableThreads)
-        row(s_long[l][0] + k, s_long[l][1], from, to, k);
+        row(s_long[l][0] + k, s_long[l][1], from, to, k, s_long[l][4], s_long[l][5]);
     }
     __syncthreads();
   }
+  if (tid == 0 && p.cuts) {
+    // (a cut sequence has one slot more than segments)
+    *(int4*)p.cuts = make_int4(min(carry_cut, p.max_cuts), min((int)(carry >> 32) - carry_cut, p.max_cut_segs), 0, 0);
+  }
   if (!sort) return;
-  const int total = min(carry, p.max_segs);
+  const int total = min((int)(uint32_t)carry, p.max_segs);
   if (tid >= total) return;
   const int4 own = s_row[tid];
   int rank = 0;
@@ -887,16 +913,21 @@ template <typename TI, int N, int P>
 __global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, int parts) {
   constexpr int VECS = N * P / 4, NT = N / 16;
   const int unit = blockIdx.x / parts, part = blockIdx.x - unit * parts;
-  const int seq = unit / p.heads, h = unit - seq * p.heads;
-  const int s0 = p.packed ? p.seg_off[seq] : seq * p.segs_per_seq;
-  const int s1 = p.packed ? p.seg_off[seq + 1] : s0 + p.segs_per_seq;
-  if (s1 - s0 < 2) return;
+  const int nth = unit / p.heads, h = unit - nth * p.heads;  // of the cut sequences
+  int seq = nth, s0 = seq * (p.segs_per_seq + 1), s1 = s0 + p.segs_per_seq;  // (s1: the end state's)
+  if (p.packed) {
+    const int4 row = *(const int4*)(p.cuts + 4 * ((int64_t)nth + 1));
+    if (nth >= p.cuts[0]) return;
+    seq = row.x;
+    s0 = row.y;
+    s1 = s0 + row.z;
+  }
   const int64_t step = (int64_t)p.heads * VECS;
   for (int at = part * kSsmJoinThreads + threadIdx.x; at < VECS; at += parts * kSsmJoinThreads) {
     f32x4* v = (f32x4*)p.slots + ((int64_t)(s0 + 1) * p.heads + h) * VECS + at;
     const float* dec = p.seg_decay + (int64_t)(s0 + 1) * p.heads + h;
     f32x4 end = zero4();
-    if (p.final_state) end = ((const f32x4*)p.ends)[(int64_t)unit * VECS + at];
+    if (p.final_state) end = v[(s1 - (s0 + 1)) * step];
     const float last = dec[(int64_t)(s1 - s0 - 2) * p.heads];
     f32x4 carry = *v;
     // a batch of slots is asked for at once (past the last one it is read again)
@@ -921,7 +952,7 @@ __global__ __launch_bounds__(kSsmJoinThreads) void ssm_join_kernel(SsmParams p, 
     if (p.final_state) {
       // the fragment's place in the state (see ssm_kernel): wave's columns, tile, lane
       const int lane = at & 63, nt = (at >> 6) % NT, wave = (at >> 6) / NT;
-      float* dst = p.final_state + ((int64_t)unit * N + ssm_state_row<TI, N>(nt, lane >> 4)) * P + 16 * wave + (lane & 15);
+      float* dst = p.final_state + (((int64_t)seq * p.heads + h) * N + ssm_state_row<TI, N>(nt, lane >> 4)) * P + 16 * wave + (lane & 15);
 #pragma unroll
       for (int j = 0; j < 4; ++j) dst[j * P] = end[j] + last * carry[j];
     }
@@ -1021,6 +1052,7 @@ static hipError_t launch_ssm_kernel(bool out, const SsmParams& p, hipStream_t s)
 template <typename TI, int N, int P>
 static hipError_t launch_ssm_np(bool out, const SsmParams& given, hipStream_t s) {
   SsmParams p = given;
+  if (!out && p.packed) p.max_segs = p.max_cut_segs;
   // heads that go to one XCD together: those of a group, unless that leaves
   // XCDs without work
   p.unit = (int64_t)p.max_segs * (p.heads / p.group) >= 64 ? p.group : 1;
@@ -1033,9 +1065,9 @@ static hipError_t launch_ssm_np(bool out, const SsmParams& given, hipStream_t s)
     e = launch_ssm_kernel<TI, N, P, 1>(out, p, s);
   }
   if (out || e != hipSuccess) return e;
-  // workgroups for every vector; where that is many, most of them of packed
-  // sequences that are not cut, fewer that go round
-  const int64_t units = (int64_t)p.n_seq * p.heads;
+  // workgroups for every vector; where that is many, most of them past the
+  // last cut sequence of a packed batch, fewer that go round
+  const int64_t units = (int64_t)p.max_cuts * p.heads;
   const int all = (N * P / 4 + kSsmJoinThreads - 1) / kSsmJoinThreads;
   const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(all, 1024 / units));
   if (units * parts > kLaunchThreads / kSsmJoinThreads) return hipErrorInvalidValue;
