@@ -500,8 +500,9 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) settle(H[nt][ct]);
   // a state that is handed on takes three terms, one that only this segment
-  // reads two
-  const bool third = !OUT || (sg.first && sg.last && p.final_state);
+  // reads two (of a sequence's only segment, whether or not the final state is
+  // asked for: its outputs are the same)
+  const bool third = !OUT || (sg.first && sg.last);
   SsmRows<TI, N> rows(lane);
   SsmCols<TI, P> cols(col0, lane);
   uint32_t l8 = lane * 8;

@@ -538,7 +538,10 @@ typedef struct gdn_ssm_options {
    * it can be cut into segments whose end states are formed at once (each
    * from zero), joined in order, and then scanned at once.  0 (default):
    * automatic; -1: one pass over each sequence; n > 0: segments of n blocks
-   * of 64 tokens (the results differ in rounding).                          */
+   * of 64 tokens.  The results differ in rounding, and the automatic choice
+   * follows the whole batch (its tokens and sequences, the heads and types);
+   * with -1 or n, a sequence's results do not depend on the others.  None
+   * depends on whether final_state is given.                                */
   int32_t segment_blocks;
 } gdn_ssm_options;
 
