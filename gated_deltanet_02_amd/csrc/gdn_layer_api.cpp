@@ -481,19 +481,21 @@ int gdn_ssm_prefill(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor*
       (rc = parse_tokens(dt, "dt", 1, &P.dt)))
     return rc;
   const int64_t epg = P.bf16 ? 8 : 4;
+  if ((rc = token_stride("x", P.P, &P.x)) || (rc = token_stride("b", P.N, &P.b)) ||
+      (rc = token_stride("c", P.N, &P.c)) || (rc = token_stride("out", P.P, &P.o)) ||
+      (rc = token_stride("dt", 1, &P.dt)))
+    return rc;
   const struct { const gdn_tensor* t; const Tokens* v; const char* n; } vecs[] = {
       {x, &P.x, "x"}, {b, &P.b, "b"}, {c, &P.c, "c"}, {out, &P.o, "out"}};
   if (P.T > 0)
     for (const auto& v : vecs) {
       if (!aligned16(v.t->data)) return api_fail(GDN_ERR_LAYOUT, "%s must be 16-byte aligned", v.n);
-      if (v.v->st % epg || v.t->stride[r - 2] % epg)
+      // (of a single head the stride is never taken either)
+      if (v.v->st % epg || (v.t->shape[r - 2] > 1 && v.t->stride[r - 2] % epg))
         return api_fail(GDN_ERR_LAYOUT, "%s: token/head strides must be multiples of %lld elements", v.n,
                         (long long)epg);
     }
-  if ((rc = check_rows("out", P.T, P.o.st, P.H, out->stride[r - 2], P.P)) || (rc = token_stride("x", P.P, &P.x)) ||
-      (rc = token_stride("b", P.N, &P.b)) || (rc = token_stride("c", P.N, &P.c)) ||
-      (rc = token_stride("out", P.P, &P.o)) || (rc = token_stride("dt", 1, &P.dt)))
-    return rc;
+  if ((rc = check_rows("out", P.T, P.o.st, P.H, out->stride[r - 2], P.P))) return rc;
   if (init_state && (rc = check_state(init_state, "init_state", P.seq.n, P))) return rc;
   if (final_state && (rc = check_state(final_state, "final_state", P.seq.n, P))) return rc;
   if (P.total > 0 && (!workspace || workspace_bytes < P.total))
@@ -611,7 +613,8 @@ int gdn_ssm_decode(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor* 
   const int64_t es = element_size(x->dtype);
   const struct { const gdn_tensor* t; const char* name; } rows[] = {{x, "x"}, {out, "out"}};
   for (const auto& v : rows)
-    if ((uintptr_t)v.t->data % (uintptr_t)(4 * es) || v.t->stride[0] % 4 || v.t->stride[1] % 4)
+    if ((uintptr_t)v.t->data % (uintptr_t)(4 * es) || (n > 1 && v.t->stride[0] % 4) ||
+        (P.H > 1 && v.t->stride[1] % 4))  // (of a single row or head the stride is never taken)
       return api_fail(GDN_ERR_LAYOUT, "%s rows must start on 4-element boundaries", v.name);
   if ((rc = check_rows("out", n, out->stride[0], P.H, out->stride[1], P.P))) return rc;
   const Range outs[2] = {range_of(out, "out"), range_of(state, "state")};

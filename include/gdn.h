@@ -482,6 +482,7 @@ int gdn_check_cu_seqlens(const int32_t* cu_host, int64_t n_seq, int64_t t_total)
  * GDN_ERR_LAYOUT, and so are output rows that overlap each other (a token or
  * head stride of zero).  All sums, norms and states are fp32, and each output
  * is rounded once.  Tokens, sequences and channels: at most 2^31 - 2^21.
+ * A dimension of one may have any stride >= 0: it is never taken.
  */
 
 /*
