@@ -214,7 +214,7 @@ int ssm_options(const gdn_ssm_options* opts, gdn_ssm_options* o) {
   return GDN_OK;
 }
 
-// Segments longer than this are cut (the chunk table counts in 32 bits).
+// The automatic choice makes no longer segments than this.
 constexpr int64_t kMaxSegment = (int64_t)1 << 20;
 int64_t ssm_groups_per_segment(const Ssm& P) {
   return P.H / gdn::ssm_group_heads(P.bf16, (int)P.P, (int)(P.H / P.G));
@@ -250,16 +250,15 @@ int64_t ssm_spread(const Ssm& P, int64_t groups) {
 // f32 39 us in 2, 56 us in 4.
 int64_t ssm_segment_tokens(const Ssm& P) {
   const int64_t block = gdn::kSsmBlock;
-  int64_t blocks;
-  if (P.opts.segment_blocks > 0) {
-    blocks = P.opts.segment_blocks;
-  } else if (P.opts.segment_blocks < 0) {
-    blocks = kMaxSegment / block;
-  } else {
-    const int64_t full = gdn::ssm_target_groups();
-    blocks = ssm_spread(P, full);
-    if (blocks < 4) blocks = std::min<int64_t>(4, std::max<int64_t>(2, ssm_spread(P, full / 2)));
+  if (P.opts.segment_blocks != 0) {
+    // as given, up to the whole of the longest sequence that there can be
+    const int64_t longest = P.seq.packed ? P.T : P.seq.len;
+    const int64_t all = std::max<int64_t>(1, (longest + block - 1) / block);
+    return (P.opts.segment_blocks < 0 ? all : std::min<int64_t>(P.opts.segment_blocks, all)) * block;
   }
+  const int64_t full = gdn::ssm_target_groups();
+  int64_t blocks = ssm_spread(P, full);
+  if (blocks < 4) blocks = std::min<int64_t>(4, std::max<int64_t>(2, ssm_spread(P, full / 2)));
   return std::min(blocks * block, kMaxSegment);
 }
 

@@ -821,7 +821,9 @@ __global__ __launch_bounds__(kSsmTableThreads) void ssm_table_kernel(SsmTable p)
     const int prev = __shfl_up(end, 1);
     const int start = max(lane > 0 ? prev : 0, before);
     end = max(end, before);
-    const int n = i < p.n_seq ? (end - start + p.seg_len - 1) / p.seg_len : 0;
+    // (unsigned: a segment may be as long as all tokens)
+    auto segments = [&](int tokens) { return (int)(((unsigned)tokens + (unsigned)p.seg_len - 1) / (unsigned)p.seg_len); };
+    const int n = i < p.n_seq ? segments(end - start) : 0;
     const bool cut = n > 1;
     const int64_t own = n + ((int64_t)(cut ? n + 1 : 0) << 32);
     const uint64_t cuts = __ballot(cut);
@@ -875,7 +877,7 @@ __global__ __launch_bounds__(kSsmTableThreads) void ssm_table_kernel(SsmTable p)
     __syncthreads();
     for (int l = 0; l < s_longs; ++l) {
       const int from = s_long[l][2], to = s_long[l][3];
-      for (int k = tid; k < (to - from + p.seg_len - 1) / p.seg_len; k += kSsmTableThreads)
+      for (int k = tid; k < segments(to - from); k += kSsmTableThreads)
         row(s_long[l][0] + k, s_long[l][1], from, to, k, s_long[l][4], s_long[l][5]);
     }
     __syncthreads();

@@ -48,3 +48,21 @@ def test_given_segments_make_sequences_independent(dtype, P, H, seg):
             o, f = run(one, [n], segment_blocks=seg)
             assert torch.equal(o, out[start: start + n]) and torch.equal(f[0], fin[i]), i
         start += n
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("packed", [True, False])
+def test_one_pass_over_a_million_tokens(dtype, packed):
+    """segment_blocks=-1 past 2^20 tokens: the bits of two calls, each one
+    segment, with the state handed on."""
+    half, T = 1 << 20, (1 << 20) + 1000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, b, c = (torch.empty(T, 1, 16, dtype=dtype, device="cuda").normal_(generator=g) for _ in range(3))
+    dt = 0.1 * torch.rand(T, 1, generator=g, device="cuda")
+    cu = U.cu_of([T]).cuda() if packed else None
+    fin, st = (torch.empty(1, 1, 16, 16, device="cuda") for _ in range(2))
+    kw = dict(softplus=False, segment_blocks=-1)
+    out, _ = G.gdn_ssm_prefill(x, dt, b, c, cu_seqlens=cu, final_state=fin, **kw)
+    one, _ = G.gdn_ssm_prefill(x[:half], dt[:half], b[:half], c[:half], final_state=st, **kw)
+    two, _ = G.gdn_ssm_prefill(x[half:], dt[half:], b[half:], c[half:], init_state=st, final_state=st, **kw)
+    assert torch.equal(out[:half], one) and torch.equal(out[half:], two) and torch.equal(fin, st)

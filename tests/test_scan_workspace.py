@@ -60,3 +60,13 @@ def test_uniform_batches(lib, B, T):
     expect(lib.gdn_ssm_workspace_size(ref(x), ref(b), None, ref(opts(segment_blocks=1)), ctypes.byref(n)), 0)
     slots = B * (-(-T // 64) + 1)
     assert n.value == up(4 * slots * 4) + slots * 4 * 64 * 32 * 4
+
+
+@pytest.mark.parametrize("T", [1 << 20, (1 << 20) + 1, 1 << 24, (1 << 31) - (1 << 21)])
+@pytest.mark.parametrize("blocks", [-1, 1 << 25, (1 << 31) - 1])
+def test_one_pass_over_long_sequences(lib, T, blocks):
+    """Nothing is cut, however long: no states, of packed ones the table."""
+    assert size(lib, T, 1, 1, 16, 16, None, blocks) == 0
+    assert size(lib, T, 1, 1, 16, 16, 3, blocks) == up(16 * 4) + up(4 * 4)
+    # and segments of that many blocks where there are more
+    assert size(lib, T, 1, 1, 16, 16, None, 1 << 14) == (0 if T == 1 << 20 else up(4 * (-(-T // (1 << 20)) + 1)) + (-(-T // (1 << 20)) + 1) * 1024)
