@@ -131,7 +131,7 @@ int parse_tokens(const gdn_tensor* t, const char* name, int rank, Tokens* v) {
   v->st = t->stride[batched ? 1 : 0];
   if (batched && t->shape[1] == 1) v->st = t->stride[0];
   if (v->T > kMaxCount) return api_fail(GDN_ERR_SHAPE, "%s: T must be at most 2^31 - 2^21", name);
-  if (batched && !is_empty(t) && t->shape[0] > 1 && t->shape[1] > 1 && t->stride[0] != t->shape[1] * t->stride[1])
+  if (batched && !is_empty(t) && t->shape[0] > 1 && t->shape[1] > 1 && t->stride[0] != (__int128)t->shape[1] * t->stride[1])
     return api_fail(GDN_ERR_LAYOUT, "%s: batch stride must equal seq_len * token stride", name);
   return GDN_OK;
 }
