@@ -23,7 +23,7 @@ namespace gdn {
 // neighbouring lanes: read as they lie they would take as long as a tile's
 // rows, so the workgroup reads them once in order and turns them in LDS.
 //
-// Measured (bf16, W = 4): 137k tokens x 6144 channels 617 us, 5.5 TB/s (a
+// Measured (bf16, W = 4): 137k tokens x 6144 channels 637 us, 5.3 TB/s (a
 // large copy reaches 4.8; 984 us in tiles of 64 with the taps read as they lie
 // and no rows on their way); 256 steps of 6144 channels 8.7 us, the launch and
 // the trips for the table, the rows and the taps.
@@ -230,10 +230,13 @@ __global__ __launch_bounds__(kConvThreads) void short_conv_kernel(ShortConvParam
       for (int i = 0; i < kConvGroup; ++i) {
         if (t + i >= t1) break;
         if (t + i >= end && seq < last) {
-          // the next sequence, or the one behind a run of empty ones
-          if (conv_cu(p, ++seq + 1) <= t + i) seq = conv_find(p, seq, last, t + i);
-          start = conv_cu(p, seq);
+          start = conv_cu(p, ++seq);
           end = conv_cu(p, seq + 1);
+          if (t + i >= end) {  // the one behind a run of empty ones
+            seq = conv_find(p, seq, last, t + i);
+            start = conv_cu(p, seq);
+            end = conv_cu(p, seq + 1);
+          }
         }
         now[i].get(rows[W - 1]);
         if (t + i - start >= W - 1) emit(t + i, rows);
@@ -589,7 +592,7 @@ hipError_t launch_add_rms_norm(bool bf16, bool vec, const NormParams& all, hipSt
   const int64_t size = bf16 ? 2 : 4;
   // What the memory-side cache (256 MiB) cannot hold between this operator
   // and its neighbours goes past the caches: 131071 rows of 6144 (5.7 GB)
-  // 994 -> 942 us, 16384 of 5120 with their neighbours 226 -> 209; below, the
+  // 994 -> 932 us, 16384 of 5120 with their neighbours 226 -> 209; below, the
   // neighbours lose what this operator gains (4096 rows 34 -> 30 us alone,
   // 59 -> 61 with them; 256 rows 6.4 -> 7.2).
   const int64_t bytes = all.rows * all.d * (size * (1 + !!all.res + !!all.res_out + !!all.out) + !!all.out_q);

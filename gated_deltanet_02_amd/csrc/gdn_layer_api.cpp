@@ -226,8 +226,10 @@ int64_t ssm_groups_per_segment(const Ssm& P) {
 // share of all blocks, less what the sequences' last segments, half full on
 // average, take (at most half the groups, since sequences that fill the chip
 // by themselves are best left whole).  Measured, 16 heads of 128 x 64 in two
-// groups: 32 prompts of 200 to 4096 tokens 262 us, equal shares 294; 8 of 200
-// to 16384 222, 290; 64 of 200 to 4096 432 whole, 490 in equal shares.
+// groups, so and in equal shares: 8 prompts of 200 to 16384 tokens 232 and 219
+// us, 16 of 200 to 4096 138 and 138, 32 257 and 250, 64 325 and 427, 128 583
+// and 582.  (The table's order came after this rule, and below 64 prompts has
+// taken what the rule gained.)
 int64_t ssm_spread(const Ssm& P, int64_t groups) {
   const int64_t block = gdn::kSsmBlock;
   const int64_t each = ssm_groups_per_segment(P);
@@ -244,10 +246,11 @@ int64_t ssm_spread(const Ssm& P, int64_t groups) {
 // the two workgroups a compute unit holds, so that a few long sequences do
 // not leave the chip idle; problems too small for segments of four blocks
 // that way, over one workgroup a compute unit, in segments of two to four
-// blocks.  Measured: 4096 tokens x 16 heads (128 x 128 states) take 48 us in
-// segments of 4 blocks, 52 us in 2 or 3, 55 us in 6; 16384 x 48 heads 303 us
-// in 26 (the choice), 313 us in 13, 391 us in 43; 1000 tokens x 8 heads of
-// f32 39 us in 2, 56 us in 4.
+// blocks.  Measured: 4096 tokens x 16 heads (128 x 128 states) take 44 us in
+// segments of 4 blocks (the choice), 50 us in 2, 51 in 3, 47 in 5, 52 in 6, 70
+// in 1; 16384 x 48 heads 291 us in 26 (the choice), 302 in 13, 386 in 43; five
+// prompts of up to 1000 tokens x 8 heads of f32 34 us in 2 (the choice), 43 in
+// 3, 51 in 4, 28 in 1.
 int64_t ssm_segment_tokens(const Ssm& P) {
   const int64_t block = gdn::kSsmBlock;
   if (P.opts.segment_blocks != 0) {

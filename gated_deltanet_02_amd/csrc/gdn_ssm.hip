@@ -15,8 +15,10 @@
 // other is fp32 and is fed as the sum of bf16 terms: two for the outputs (M
 // and S; 2^-16 of a product, below the output's own rounding), three for the
 // state where it is handed on (w_t x_t; 2^-24, so the fp32 state keeps fp32
-// accuracy) and two where only this segment's outputs read it.  fp32 inputs
-// use fp32 matrix instructions throughout.  Sums of steps are run in fp64.
+// accuracy) and two where only this segment's outputs read it: bf16 outputs
+// differ from those of fp32 products in 1e-4 (their own rounding: 1.7e-3).
+// fp32 inputs use fp32 matrix instructions throughout (1.3e-7 from 64 bits, as
+// a plain fp32 evaluation).  Sums of steps are run in fp64.
 //
 // A workgroup of eight waves scans one segment of one 128-column head or of
 // two 64-column ones (fewer waves for fewer columns), in blocks of C = 32
@@ -34,19 +36,18 @@
 // order, and the scan of all segments at once.
 //
 // What bounds it: not the bytes (16384 tokens x 48 heads of 128 x 128 in
-// bf16: 546 MB in 300 us, 1.8 TB/s) nor LDS (44 % busy; tiles laid out with
-// half the bank conflicts took as long), but issue.  A wave issues about 243
-// vector instructions and 38 matrix ones a block, 96 of the former to split
-// the state into terms; a matrix instruction of 16 cycles lets two vector
-// instructions of other waves in where four would fit (both measured), so
-// the two together take about 75 % of a SIMD's cycles (counters: vector unit
-// 60 %, matrix cores 31 %), and the block's barrier the rest.  Measured on
-// that case: 16 columns a wave in blocks of 32 (128 registers, two
-// workgroups a compute unit), 305 us, against 496 for 32 columns in blocks of
-// 64 (one workgroup); two blocks a barrier for the segments' states and
-// batched joining, 291.  No faster: copies by a ninth wave, ageing the state
-// less often, raised priority for the matrix phases, deeper rings, the split
-// by dot products (they take the matrix unit's slots).
+// bf16: 546 MB in 294 us, 288 to 306 over several cards, 1.9 TB/s) nor LDS
+// (45 % busy; tiles laid out with half the bank conflicts took as long), but
+// issue.  A wave issues about 256 vector instructions and 38 matrix ones a
+// block, 96 of the former to split the state into terms; a matrix instruction
+// of 16 cycles lets two vector instructions of other waves in where four would
+// fit (both measured), so the two together take about 75 % of a SIMD's cycles
+// (counters: vector unit 62 %, matrix cores 32 %), and the block's barrier the
+// rest.  Two blocks a barrier for the segments' states and batched joining
+// took that case from 305 to 291 us when they were built.  No faster: copies by
+// a ninth wave, ageing the state less often, raised priority for the matrix
+// phases, deeper rings, the split by dot products (they take the matrix unit's
+// slots).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -779,8 +780,9 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
 // [previous end, T], so that a malformed table can only give wrong results.
 // One workgroup, a sequence per thread and round, the scans over waves by
 // shuffles; each thread writes its own sequence's rows, or, of a sequence of
-// many segments, all threads do.  Bound by its two trips to memory and four
-// barriers (5 us for 64 prompts).
+// many segments, all threads do.  Sequences of two or more segments are
+// counted in the same scan and listed with their segments once more.  Bound by
+// its two trips to memory and four barriers (4.0 to 5.5 us for 64 prompts).
 //
 // Up to kSsmSort segments are put in the order of their lengths.  Workgroups
 // take a place in every compute unit before any takes a second one: where two
@@ -788,7 +790,7 @@ __global__ __launch_bounds__((SsmShape<TI, N, P, HP, OUT>::THREADS), (sizeof(TI)
 // them up, and the rest from the longest of them down, so that the longest
 // share a compute unit with the shortest (or with none); else the longest go
 // first.  64 prompts of 200 to 4096 tokens x 16 heads of 64 columns: 430 -> 325
-// us; 128 of them 765 -> 583.
+// us when it was built; 128 of them 765 -> 583.
 constexpr int kSsmTableThreads = 1024;
 constexpr int kSsmSort = 512;
 
@@ -909,7 +911,7 @@ hipError_t launch_ssm_table(const SsmTable& p, hipStream_t s) {
 // that one; after the last, the final state.  A thread takes four elements of
 // a (sequence, head) state; `parts` workgroups share the vecs of one.  The
 // order is a chain, so eight slots are asked for at once: bound by that trip
-// to memory (16 heads x 16 segments 6.7 us, 48 heads x 10 segments 10 us).
+// to memory (16 heads x 16 segments 6.8 us, 48 heads x 10 segments 9.9 us).
 constexpr int kSsmJoinThreads = 256;
 
 template <typename TI, int N, int P>
@@ -1035,6 +1037,13 @@ __global__ __launch_bounds__((SsmStepShape<N, P>::NT)) void ssm_step_kernel(SsmS
 // ---------------------------------------------------------------------------
 // dispatch
 
+// Two workgroups for each compute unit, what LDS and registers hold of eight
+// waves with N = 128 (one with f32 inputs and P = 128).  Where more or fewer
+// would fit the same number serves: 16384 tokens x 16 heads in segments for
+// 256, 512 (the choice) and 1024 workgroups take, in us, bf16 128 x 128 117,
+// 115, 138; 128 x 64 in odd groups 95, 78, 95, in even ones 77, 78, 101; 128 x
+// 32 105, 72, 87; 128 x 16 125, 79, 89; 16 x 128 72, 67, 73; 16 x 16 84, 55, 50
+// (54 for 2048); f32 64 x 32 152, 97, 111; f32 128 x 128 297, 316, 353.
 int ssm_target_groups() { return 512; }
 // Two heads of 64 columns fill a workgroup of eight waves.
 int ssm_group_heads(bool bf16, int p, int group) { return bf16 && p == 64 && group % 2 == 0 ? 2 : 1; }
