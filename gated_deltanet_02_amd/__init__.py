@@ -19,3 +19,5 @@ from ._binding import (GdnError, GdnOptions, GdnTensor, GdnWorkspaceLayout,  # n
 from ._binding import GraphCache, PreparedPrefill  # noqa: F401,E402
 from ._layer import (GdnSsmOptions, gdn_add_rms_norm, gdn_short_conv, gdn_ssm_decode,  # noqa: F401,E402
                      gdn_ssm_default_options, gdn_ssm_prefill, gdn_ssm_workspace_size, ssm_workspace)
+from ._attn import (GdnAttnOptions, attn_workspace, gdn_attn_decode, gdn_attn_default_options,  # noqa: F401,E402
+                    gdn_attn_prefill, gdn_attn_workspace_size, gdn_cache_plan, gdn_cache_release, gdn_cache_store)

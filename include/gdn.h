@@ -61,7 +61,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 10
+#define GDN_ABI_VERSION 11
 
 /* Status codes. */
 #define GDN_OK 0
@@ -617,6 +617,130 @@ int gdn_ssm_decode(const gdn_tensor* x, const gdn_tensor* dt, const gdn_tensor* 
 int gdn_add_rms_norm(const gdn_tensor* x, const gdn_tensor* residual, const float* weight,
                      float eps, gdn_tensor* residual_out, gdn_tensor* out, gdn_tensor* out_q,
                      gdn_tensor* scales, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The attention layers that a hybrid model has between its recurrent ones,
+ * over a paged key-value cache.  The conventions are those of the operators
+ * above.  A cache is two arrays [pages, page_size, Hk, d] (any strides that
+ * 16-byte accesses fit, so that page-major, head-major and interleaved pools
+ * all do); slot s is place s % page_size of page s / page_size.  Row i of a
+ * block table [N, M] int32 names the pages that hold request i's tokens in
+ * order: its token p lies in page block_table[i][p / page_size].  Entries
+ * behind the pages that a request's length needs are not read.  A page
+ * outside the cache, inside that length, holds no token that is seen; lengths
+ * below 0 or past M * page_size count as those.  page_size is 1 or more,
+ * M * page_size and the tokens at most 2^31 - 2^21, requests at most 2^24.
+ */
+
+/*
+ * gdn_cache_plan -- block tables and slot maps on the device, from the
+ * requests' lengths.  Request i has ctx_lens[i] tokens in the cache and the
+ * new ones of cu_seqlens (one each without it).  It holds the first
+ * ceil(ctx / page_size) pages of its row of the table, and takes what
+ * ceil((ctx + new) / page_size) needs more off the top of the stack
+ * free_pages[0 .. n_free), from the highest index down, request by request:
+ * all of its pages or, if the stack or its row of the table has not that
+ * many, none (so does then every later request that needs any from the
+ * stack).
+ *   block_table  [N, M] int32, in place: only entries of taken pages are
+ *                written
+ *   seq_lens     [N] int32: ctx + new, or ctx where a request got no pages
+ *                (may be ctx_lens)
+ *   slots        [T] int64: each new token's slot; -1 for those of a request
+ *                that got no pages and those in no sequence
+ *   n_free_out   [1] int32: what is left on the stack (may be n_free)
+ * ctx_lens [N], free_pages [F], n_free [1] are int32; all contiguous, the
+ * table's row stride any.  A count n_free outside 0 .. F counts as those.
+ */
+int gdn_cache_plan(const gdn_tensor* ctx_lens, const gdn_tensor* cu_seqlens,
+                   gdn_tensor* block_table, const gdn_tensor* free_pages,
+                   const gdn_tensor* n_free, int32_t page_size, gdn_tensor* seq_lens,
+                   gdn_tensor* slots, gdn_tensor* n_free_out, void* stream);
+
+/*
+ * gdn_cache_release -- the pages of the requests with done[i] != 0 back onto
+ * the stack, in the order of the requests and of their pages; their lengths
+ * become 0 and their entries -1.  Pages past the end of free_pages [F] are
+ * dropped.  A page belongs to one request.  done, seq_lens [N], block_table
+ * [N, M], free_pages [F], n_free [1]: int32, the last four in place.
+ */
+int gdn_cache_release(const gdn_tensor* done, gdn_tensor* seq_lens, gdn_tensor* block_table,
+                      gdn_tensor* free_pages, gdn_tensor* n_free, int32_t page_size,
+                      void* stream);
+
+/*
+ * gdn_cache_store -- rows of new keys and values into their slots.
+ *   k, v              [T, Hk, d]; bf16 or f32, unit stride in d, other strides
+ *                     multiples of 16 bytes
+ *   slots             [T] int64, as gdn_cache_plan gives them; those below 0
+ *                     or past the cache are not stored.  No slot twice (of two
+ *                     rows either one's elements may stay)
+ *   k_cache, v_cache  [pages, page_size, Hk, d] of the same dtype; they may
+ *                     interleave in one allocation
+ * d in {64, 128, 256}.
+ */
+int gdn_cache_store(const gdn_tensor* k, const gdn_tensor* v, const gdn_tensor* slots,
+                    gdn_tensor* k_cache, gdn_tensor* v_cache, void* stream);
+
+/*
+ * Attention.  The query at place p of its sequence sees the keys j <= p, with
+ * a window w > 0 only those of j > p - w or j < sinks:
+ *     out[t, h] = sum_j softmax_j(scale q[t, h].k_j) v_j
+ * over the keys it sees, query head h reading key head h / (H/Hk); a row that
+ * sees none is 0.  Scores, the softmax's maximum and sum and the output are
+ * held in fp32, and the output is rounded once; with bf16 inputs the weights
+ * enter the product with v in bf16 (prompts: one term; single tokens: two).
+ * Inputs of what is seen are expected to be finite: a NaN or infinity in a
+ * key or value reaches the rows that see it and may reach earlier rows of its
+ * own sequence in the same tile of 256; none reaches another sequence, and
+ * what lies in the cache behind a sequence's length is never read.
+ */
+typedef struct gdn_attn_options {
+  float scale;     /* multiplies the scores; 0 (default): 1 / sqrt(d)         */
+  int32_t window;  /* keys that a query sees, its own among them; 0: all      */
+  int32_t sinks;   /* first tokens that every query sees beside its window    */
+} gdn_attn_options;
+
+/* Fills *opts with the defaults listed in gdn_attn_options. */
+void gdn_attn_default_options(gdn_attn_options* opts);
+
+/*
+ * gdn_attn_prefill -- attention of prompts.
+ *   q, out      [T, H, d] or [B, T/B, H, d]; bf16 or f32
+ *   cu_seqlens  as gdn_prefill; rows at or after cu[N] are not written
+ *   k, v        without a block table [T, Hk, d] (or 4-D as q): the queries'
+ *               own tokens are the whole sequences.  With one, the caches: the
+ *               queries are the last tokens of the first seq_lens[i] that the
+ *               cache holds of sequence i (the new ones stored already), so
+ *               that a prompt can come in chunks or continue what is cached; a
+ *               query before a sequence's first token sees none
+ *   block_table, seq_lens  [N, M], [N] int32, or both NULL
+ *   opts        NULL for the defaults
+ * d in {64, 128, 256}; unit stride in d, other strides multiples of 16 bytes.
+ */
+int gdn_attn_prefill(const gdn_tensor* q, const gdn_tensor* k, const gdn_tensor* v,
+                     const gdn_tensor* cu_seqlens, const gdn_tensor* block_table,
+                     const gdn_tensor* seq_lens, gdn_tensor* out, const gdn_attn_options* opts,
+                     void* stream);
+
+/*
+ * gdn_attn_decode -- attention of one new token for each of N sequences, the
+ * last of the seq_lens[i] that the cache holds (the new one stored already).
+ *   q, out     [N, H, d]; bf16 or f32
+ *   workspace  gdn_attn_workspace_size() bytes of device memory, 256-byte
+ *              aligned; not to be used by another call that overlaps on the
+ *              device.  It follows q's dtype and d alone
+ * The work is shared out in equal parts over the device, whatever the
+ * lengths, and parts of one sequence are joined by a second launch: the last
+ * bits of a result depend on the whole batch's lengths.
+ */
+int gdn_attn_decode(const gdn_tensor* q, const gdn_tensor* k_cache, const gdn_tensor* v_cache,
+                    const gdn_tensor* block_table, const gdn_tensor* seq_lens, gdn_tensor* out,
+                    const gdn_attn_options* opts, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Workspace bytes of gdn_attn_decode for a q of this dtype and d (host only). */
+int gdn_attn_workspace_size(const gdn_tensor* q, size_t* bytes);
 
 /* Short description of a status code (static storage). */
 const char* gdn_status_string(int status);
