@@ -2,6 +2,19 @@
 // gfx950: out = softmax(scale q.k) v over the keys that a query sees, those
 // at or before its place and, with a window, inside it or among the first
 // `sinks`.
+//
+// Both run over tiles of keys with the running maximum m and sum l of a
+// row's softmax: s = scale log2(e) q.k, m' = max(m, s), l <- 2^(m - m') l +
+// sum 2^(s - m'), O <- 2^(m - m') O + sum 2^(s - m') v, out = O / l.  The
+// products are formed transposed, S^T = K Q^T and O^T = V^T P^T: a query is
+// then a lane's column in both, so that m, l and the rescaling are one
+// value a lane, and S^T's accumulators, whose rows are keys, are P^T's
+// operand as they stand.  V^T's operand comes from LDS by transposed reads.
+//
+// Keys and values are copied straight to LDS, row by row from wherever their
+// page lies.  Rows that no query of the tile sees (behind the sequence's end,
+// outside the window, in a page that is not there) are copied from a zero, so
+// that whatever the cache holds there reaches no product.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -13,6 +26,8 @@ namespace gdn {
 
 namespace {
 
+__device__ const uint32_t attn_zeros[4] = {0u, 0u, 0u, 0u};
+
 __device__ __forceinline__ int attn_quotient(const Divide& d, int n) {
   return (int)((__umulhi(d.mul, (uint32_t)n) + (uint32_t)n) >> d.shift);
 }
@@ -22,103 +37,646 @@ __device__ __forceinline__ int attn_cu(const AttnParams& p, int64_t i) {
   return (int)min(max(v, (int64_t)0), (int64_t)p.t_total);
 }
 
-// One wave a row and head: lanes share a row's d, keys one after the other.
-template <typename TI, int D, bool STEP>
-__global__ __launch_bounds__(256) void attn_plain(AttnParams p) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t t = item / p.heads;
-  const int h = (int)(item - t * p.heads);
-  if (t >= p.t_total) return;
-  int seq, place, start = 0;
-  if (STEP) {
-    seq = (int)t;
-    place = min(max(p.lens[seq], 0), p.max_len) - 1;
-  } else {
-    int end;
-    if (p.cu) {
-      int lo = 0, hi = p.n_seq - 1;
-      while (lo < hi) {
-        const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
-        if (attn_cu(p, mid) <= t) lo = mid;
-        else hi = mid - 1;
-      }
-      seq = lo;
-      start = attn_cu(p, seq);
-      end = attn_cu(p, seq + 1);
-    } else {
-      seq = (int)(t / p.seq_len);
-      start = seq * p.seq_len;
-      end = start + p.seq_len;
-    }
-    if (t < start || t >= end) return;
-    place = (int)t - start;
-    if (p.table) place += min(max(p.lens[seq], 0), p.max_len) - (end - start);
-  }
-  const char* q = (const char*)p.q + t * p.q_st + h * p.q_sh;
-  float qv[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = to_float(((const TI*)q)[lane + 64 * e]);
-    o[e] = 0.f;
-  }
-  const int kh = h / p.group;
-  for (int j = 0; j <= place; ++j) {
-    if (p.window > 0 && place - j >= p.window && j >= p.sinks) {
-      j = place - p.window;
-      continue;
-    }
-    const char *kr, *vr;
-    if (p.table) {
-      const int c = attn_quotient(p.page, j), in = j - c * (int)p.page.d;
-      const int page = p.table[seq * p.table_st + c];
-      if (page < 0 || page >= p.pages) continue;
-      kr = (const char*)p.k + page * p.k_sp + in * p.k_st;
-      vr = (const char*)p.v + page * p.v_sp + in * p.v_st;
-    } else {
-      kr = (const char*)p.k + (int64_t)(start + j) * p.k_st;
-      vr = (const char*)p.v + (int64_t)(start + j) * p.v_st;
-    }
-    kr += kh * p.k_sh;
-    vr += kh * p.v_sh;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += qv[e] * to_float(((const TI*)kr)[lane + 64 * e]);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    s *= p.scale;
-    const float top = fmaxf(m, s), old = __builtin_amdgcn_exp2f(m - top), w = __builtin_amdgcn_exp2f(s - top);
-    m = top;
-    l = l * old + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * old + w * to_float(((const TI*)vr)[lane + 64 * e]);
-  }
-  TI* out = (TI*)((char*)p.out + t * p.o_st + h * p.o_sh);
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[lane + 64 * e] = from_float<TI>(l > 0.f ? o[e] / l : o[e]);
+// A length that is the same for all lanes, through the scalar cache (nothing
+// writes the lengths meanwhile), so that the copies under way are not waited
+// for.
+__device__ __forceinline__ int attn_len(const AttnParams& p, int seq) {
+  typedef const __attribute__((address_space(4))) int32_t* constant;
+  const int v = ((constant)(uintptr_t)p.lens)[seq];
+  return min(max(v, 0), p.max_len);
 }
 
-template <bool STEP>
-hipError_t launch_plain(bool bf16_in, int d, const AttnParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)p.t_total * p.heads + 3) / 4)), threads(256);
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, threads, 0, s, p); };
-  if (d == 64) bf16_in ? go(attn_plain<bf16, 64, STEP>) : go(attn_plain<float, 64, STEP>);
-  else if (d == 128) bf16_in ? go(attn_plain<bf16, 128, STEP>) : go(attn_plain<float, 128, STEP>);
-  else bf16_in ? go(attn_plain<bf16, 256, STEP>) : go(attn_plain<float, 256, STEP>);
+// Copies of 16 or 4 bytes a lane into LDS, each lane's from its own address,
+// in the order of the lanes from `lds` on.  Written as assembly so that the
+// compiler does not wait for them at every LDS read: the wave counts them and
+// waits itself.
+__device__ __forceinline__ void attn_copy16(uint32_t lds, const void* from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"((uint64_t)(uintptr_t)from)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void attn_copy4(uint32_t lds, const void* from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"((uint64_t)(uintptr_t)from)
+               : "memory", "m0");
+}
+
+__device__ __forceinline__ uint32_t attn_lds(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+
+// Waits until at most n copies (and other global accesses) are under way.
+template <int N>
+__device__ __forceinline__ void attn_wait() {
+  static_assert(N <= 63, "more than the wave counts");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(ssm_vmcnt(N));
+  asm volatile("" ::: "memory");
+}
+// Waits for this wave's LDS reads.
+__device__ __forceinline__ void attn_wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+  asm volatile("" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// 16 queries of a wave against tiles of 16 TT keys
+
+template <typename TI, int D, int TT>
+struct AttnCore {
+  static constexpr int S = sizeof(TI), RB = D * S, GR = RB / 16;
+  static constexpr int NU = RB / 64;  // operand units along d
+  static constexpr int NC = D / 16;   // column tiles of O
+  using U = typename Unit<TI>::type;
+  U q[NU];
+  f32x4 o[NC];  // O^T: d 16 i + 4 (l / 16) + e, query l % 16
+  float m, l;   // l: this lane's keys alone
+
+  __device__ __forceinline__ void reset() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) o[i] = zero4();
+  }
+  // the queries' rows, or zeros
+  __device__ __forceinline__ void load(const char* row, bool live, int lane) {
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (live) v = ld16(row + (4 * u + (lane >> 4)) * 16);
+      q[u] = __builtin_bit_cast(U, v);
+    }
+  }
+  // s[t][e]: key 16 t + 4 (l / 16) + e, query l % 16
+  __device__ __forceinline__ void scores(const char* k, f32x4 (&s)[TT], int lane) const {
+    const int r = lane & 15, g = lane >> 4;
+    const uint32_t at = r * RB + ((g ^ ssm_swz<GR>(r)) * 16);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) s[t] = zero4();
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const U a = *(const U*)(k + (at ^ (u * 64)) + t * 16 * RB);
+        mma_unit<false>(s[t], a, q[u]);
+      }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) settle(s[t]);
+  }
+  // Takes a tile of scores in: s becomes the weights.
+  __device__ __forceinline__ void weigh(f32x4 (&s)[TT]) {
+    float top = s[0][0];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, s[t][e]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    top = fmaxf(m, top);
+    // (a row that has seen nothing yet: weights of 2^-inf)
+    const float from = top == -INFINITY ? 0.f : top;
+    const float keep = __builtin_amdgcn_exp2f(m - from);
+    m = top;
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[t][e] = __builtin_amdgcn_exp2f(s[t][e] - from);
+        sum += s[t][e];
+      }
+    l = l * keep + sum;
+    if (__any(keep != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= keep;
+    }
+  }
+  // O^T += V^T P^T; bf16 weights as two terms, hi and what it leaves, which
+  // cost nothing where memory is waited for: within 2^-16 of the weight.
+  __device__ __forceinline__ void add(const char* v, const f32x4 (&s)[TT], int lane) {
+    const SsmCols<TI, D> cols(0, lane);
+    if constexpr (S == 2) {
+      static_assert(TT == 2, "two key tiles an operand unit");
+      bf16x8 hi, lo;
+      ssm_split2<false>(s[0], s[1], hi, lo);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const bf16x8 a = cols.column(v, i, 0);
+        mma_unit<false>(o[i], a, hi);
+        mma_unit<false>(o[i], a, lo);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) mma_unit<false>(o[i], cols.column(v, i, t), s[t]);
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) settle(o[i]);
+  }
+  // the whole sum of the row's weights
+  __device__ __forceinline__ float total() const {
+    float a = l;
+    a += __shfl_xor(a, 16);
+    a += __shfl_xor(a, 32);
+    return a;
+  }
+  __device__ __forceinline__ void store(char* row, int lane) const {
+    const float sum = total(), inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+    if (!row) return;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      store4<TI>((TI*)row + 16 * i + 4 * (lane >> 4), o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// single tokens
+//
+// The queries of a key head's group (16 at most at a time) are a tile's
+// columns, and memory is all that counts: every key and value once.  All
+// tiles of all (sequence, key head) pairs are one list, cut in equal parts
+// over the waves, so that ragged lengths, one long sequence or many short ones
+// load the chip alike.  A wave works by itself, without barriers: its ring in
+// LDS holds two tiles of keys and of values, the next under way while one is
+// used, and the table's entries of the one after.  A wave whose part ends
+// inside a pair leaves m, l and O to the join.
+
+template <typename TI, int D>
+struct StepShape {
+  static constexpr int TT = sizeof(TI) == 2 ? 2 : 1, TW = 16 * TT;  // keys of a tile
+  static constexpr int RB = D * (int)sizeof(TI), GR = RB / 16, TILE = TW * RB;
+  static constexpr int NW = 131072 / (4 * TILE);  // waves of a workgroup
+  static constexpr int PIECES = TW * GR / 64;     // copies of a tile
+  static constexpr int ring = 4 * TILE, entries = NW * ring, total = entries + NW * 2 * 256;
+  static_assert(total <= 163840 && NW >= 1 && NW <= 16, "LDS");
+};
+
+// A tile of the list: its pair, the first of its keys among those that the
+// sequence's query sees, and how many those are.
+struct StepTile {
+  int seq, unit, tile, tiles;
+  int seen, gap;  // keys from `sinks` on lie `gap` further behind
+};
+
+struct StepWork {
+  const AttnParams& p;
+  int units, blocks, keys;
+  __device__ __forceinline__ int seen(int len) const {
+    return p.window > 0 ? (int)min((int64_t)len, (int64_t)p.window + p.sinks) : len;
+  }
+  __device__ __forceinline__ int tiles(int len) const { return (seen(len) + keys - 1) / keys; }
+  __device__ __forceinline__ int lane_len(int64_t i) const {
+    return i < p.n_seq ? min(max(p.lens[i], 0), p.max_len) : 0;
+  }
+  __device__ __forceinline__ void enter(StepTile& x, int seq) const {
+    const int len = attn_len(p, seq);
+    x.seq = seq;
+    x.seen = seen(len);
+    x.gap = len - x.seen;
+    x.tiles = (x.seen + keys - 1) / keys;
+  }
+  // The next tile of the list (there is one).
+  __device__ __forceinline__ void next(StepTile& x, int lane) const {
+    if (++x.tile < x.tiles) return;
+    x.tile = 0;
+    if (++x.unit < units) return;
+    x.unit = 0;
+    int seq = x.seq + 1;
+    if (attn_len(p, seq) == 0) {  // empty ones, 64 at a time
+      uint64_t some;
+      while ((some = __ballot(lane_len((int64_t)seq + lane) > 0)) == 0) seq += 64;
+      seq += __ffsll((unsigned long long)some) - 1;
+    }
+    enter(x, __builtin_amdgcn_readfirstlane(seq));
+  }
+};
+
+__device__ __forceinline__ int64_t wave_upto(int64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ int64_t wave_pick(int64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+template <typename TI, int D>
+__global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnParams p) {
+  using H = StepShape<TI, D>;
+  constexpr int TT = H::TT, TW = H::TW, RB = H::RB, GR = H::GR, P = H::PIECES;
+  __shared__ __attribute__((aligned(1024))) char smem[H::total];
+  const int lane = threadIdx.x & 63;
+  const int in_group = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave = blockIdx.x * H::NW + in_group;
+  char* ring = smem + in_group * H::ring;                 // two stages of keys, then values
+  const int* entries = (const int*)(smem + H::entries + in_group * 512);
+  const uint32_t ring_at = attn_lds(ring), entries_at = attn_lds(entries);
+
+  StepWork w{p, 0, (p.group + kDecodeHeads - 1) / kDecodeHeads, TW};
+  w.units = p.kv * w.blocks;
+
+  // the wave's part [a, b) of the list: lane l sums the tiles of the sequences
+  // [l c, (l + 1) c), c a 64th of all
+  const int64_t c = ((int64_t)p.n_seq + 63) / 64;
+  int64_t sum = 0;
+  for (int64_t i = lane * c; i < (lane + 1) * c; ++i) sum += w.tiles(w.lane_len(i));
+  const int64_t upto = wave_upto(sum, lane);
+  const int64_t all = wave_pick(upto, 63) * w.units;
+  const int64_t each = all / p.waves, more = all - each * p.waves;
+  const int64_t a = wave * each + min((int64_t)wave, more), b = a + each + (wave < more ? 1 : 0);
+  int chain = 0, chain_seq = 0, chain_unit = 0;
+
+  if (a < b) {
+    StepTile x;
+    int64_t first;  // of the pair's tiles
+    {
+      const uint64_t past = __ballot(upto * w.units > a);
+      const int at = __ffsll((unsigned long long)past) - 1;
+      int64_t before = wave_pick(upto - sum, at);
+      int64_t i0 = at * c;
+      int64_t mine, inner;
+      uint64_t hit;
+      for (;;) {  // the sequence among the lane's, 64 at a time
+        mine = i0 + lane < (at + 1) * c ? w.tiles(w.lane_len(i0 + lane)) : 0;
+        inner = wave_upto(mine, lane);
+        hit = __ballot((before + inner) * w.units > a);
+        if (hit) break;
+        before += wave_pick(inner, 63);
+        i0 += 64;
+      }
+      const int k = __ffsll((unsigned long long)hit) - 1;
+      before += wave_pick(inner - mine, k);
+      w.enter(x, __builtin_amdgcn_readfirstlane((int)(i0 + k)));
+      const int64_t rest = a - before * w.units;
+      x.unit = __builtin_amdgcn_readfirstlane((int)(rest / x.tiles));
+      x.tile = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)x.unit * x.tiles));
+      first = a - x.tile;
+    }
+
+    // The table's entries of a tile, one a lane, into one of two rows.
+    const auto place = [&](const StepTile& t, int i) { return i < p.sinks || t.gap == 0 ? i : i + t.gap; };
+    const auto ask = [&](const StepTile& t, bool live, int row) {
+      const int i = t.tile * TW + lane;
+      const void* from = p.lens;
+      if (live && lane < TW && i < t.seen)
+        from = p.table + t.seq * p.table_st + attn_quotient(p.page, place(t, i));
+      attn_copy4(entries_at + row * 256, from);
+    };
+    // The keys, then the values of a tile whose entries have come; which of
+    // its keys there are.
+    const auto fetch = [&](const StepTile& t, bool live, int row, int stage) -> uint32_t {
+      const int i = t.tile * TW + lane;
+      int page = -1, in = 0;
+      if (live && lane < TW && i < t.seen) {
+        const int at = place(t, i);
+        page = entries[row * 64 + lane];
+        if ((uint32_t)page >= (uint32_t)p.pages) page = -1;
+        in = at - attn_quotient(p.page, at) * (int)p.page.d;
+      }
+      const uint32_t there = (uint32_t)__ballot(page >= 0);
+      const int kh = t.unit / w.blocks;
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        const char* base = kind ? (const char*)p.v + kh * p.v_sh : (const char*)p.k + kh * p.k_sh;
+        const int64_t sp = kind ? p.v_sp : p.k_sp, st = kind ? p.v_st : p.k_st;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const int r = j * (64 / GR) + lane / GR;
+          const int pg = __shfl(page, r), pl = __shfl(in, r);
+          const char* from = base + pg * sp + pl * st + (((lane % GR) ^ ssm_swz<GR>(r)) * 16);
+          attn_copy16(ring_at + (2 * stage + kind) * H::TILE + j * 1024, pg >= 0 ? from : (const char*)attn_zeros);
+        }
+      }
+      return there;
+    };
+
+    StepTile now = x, then = x;
+    uint32_t there, there_then = 0;
+    ask(x, true, 0);
+    attn_wait<0>();
+    there = fetch(now, true, 0, 0);
+    if (a + 1 < b) w.next(x, lane);
+    then = x;
+    ask(x, a + 1 < b, 1);
+    AttnCore<TI, D, TT> core;
+    bool fresh = true;
+    for (int64_t t = a; t < b; ++t) {
+      const int stage = (int)(t - a) & 1;
+      // entries of the tile after the next
+      if (t + 2 < b) w.next(x, lane);
+      attn_wait_lds();
+      ask(x, t + 2 < b, stage);
+      attn_wait<1>();  // this tile, and the next one's entries
+      there_then = fetch(then, t + 1 < b, stage ^ 1, stage ^ 1);
+      const int kh = now.unit / w.blocks, h0 = kh * p.group + (now.unit - kh * w.blocks) * kDecodeHeads;
+      const int heads = min(kDecodeHeads, (kh + 1) * p.group - h0);
+      const int r = lane & 15;
+      if (fresh) {
+        core.reset();
+        core.load((const char*)p.q + now.seq * p.q_st + (h0 + r) * p.q_sh, r < heads, lane);
+        fresh = false;
+      }
+      f32x4 s[TT];
+      core.scores(ring + 2 * stage * H::TILE, s, lane);
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[k][e] *= p.scale;
+      if (there != (TW == 32 ? 0xffffffffu : 0xffffu)) {
+#pragma unroll
+        for (int k = 0; k < TT; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[k][e] = (there >> (16 * k + 4 * (lane >> 4) + e)) & 1u ? s[k][e] : -INFINITY;
+      }
+      core.weigh(s);
+      core.add(ring + (2 * stage + 1) * H::TILE, s, lane);
+      if (now.tile + 1 == now.tiles || t + 1 == b) {
+        fresh = true;
+        if (first >= a && now.tile + 1 == now.tiles) {
+          core.store(r < heads ? (char*)p.out + now.seq * p.o_st + (h0 + r) * p.o_sh : nullptr, lane);
+        } else {
+          // a part: of a pair begun here the second slot
+          const bool begun = first >= a;
+          float* part = p.parts + (2 * (int64_t)wave + (begun ? 1 : 0)) * attn_part_floats(D);
+          const float sum = core.total();
+          if (r < heads) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) *(f32x4*)(part + r * D + 16 * i + 4 * (lane >> 4)) = core.o[i];
+            if (lane < 16) {
+              part[16 * D + r] = core.m;
+              part[16 * D + 16 + r] = sum;
+            }
+          }
+          if (begun) {
+            // the wave of the pair's last tile
+            const int64_t end = first + now.tiles - 1;
+            const int64_t last = end < more * (each + 1) ? end / (each + 1) : more + (end - more * (each + 1)) / each;
+            chain = (int)(last - wave) + 1;
+            chain_seq = now.seq;
+            chain_unit = now.unit;
+          }
+        }
+        first += now.tiles;
+      }
+      now = then;
+      then = x;
+      there = there_then;
+    }
+    attn_wait<0>();  // no copy may land after the workgroup's end
+  }
+  if (lane == 0) ((int4*)p.chains)[wave] = make_int4(chain, chain_seq, chain_unit, 0);
+  // sequences that hold nothing
+  for (int64_t i = wave; i < p.n_seq; i += p.waves) {
+    if (attn_len(p, (int)i) != 0) continue;
+    for (int g = lane; g < p.heads * GR; g += 64)
+      st16((char*)p.out + i * p.o_st + (g / GR) * p.o_sh + (g % GR) * 16, make_uint4(0u, 0u, 0u, 0u));
+  }
+}
+
+// Joins the parts of one wave's chain, a head a workgroup: threads of a part
+// share the head's d in fours.
+template <typename TI, int D>
+__global__ __launch_bounds__(256) void join_kernel(AttnParams p) {
+  constexpr int W = D / 4, PG = 256 / W;
+  __shared__ f32x4 s_o[256];
+  __shared__ float s_l[PG], s_m[4];
+  const int wave = blockIdx.x, r = blockIdx.y;
+  const int4 c = ((const int4*)p.chains)[wave];
+  const int n = c.x;
+  if (n == 0) return;
+  const int blocks = (p.group + kDecodeHeads - 1) / kDecodeHeads;
+  const int kh = c.z / blocks, h = kh * p.group + (c.z - kh * blocks) * kDecodeHeads + r;
+  if (h >= (kh + 1) * p.group) return;
+  const int tid = threadIdx.x, g = tid / W, x = tid % W;
+  // part 0 is the wave's second slot, the others are the next waves' first
+  const auto part = [&](int i) { return p.parts + (2 * (int64_t)(wave + i) + (i == 0 ? 1 : 0)) * attn_part_floats(D); };
+  float m = -INFINITY;
+  for (int i = tid; i < n; i += 256) m = fmaxf(m, part(i)[16 * D + r]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  if ((tid & 63) == 0) s_m[tid >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  if (m == -INFINITY) m = 0.f;  // (no part sees anything)
+  f32x4 o = zero4();
+  float l = 0.f;
+  for (int i = g; i < n; i += PG) {
+    const float* q = part(i);
+    const float w = __builtin_amdgcn_exp2f(q[16 * D + r] - m);
+    const f32x4 v = *(const f32x4*)(q + r * D + 4 * x);
+    l += w * q[16 * D + 16 + r];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += w * v[e];
+  }
+  s_o[tid] = o;
+  if (x == 0) s_l[g] = l;
+  __syncthreads();
+  if (g == 0) {
+    for (int k = 1; k < PG; ++k) {
+      l += s_l[k];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += s_o[k * W + x][e];
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    store4<TI>((TI*)((char*)p.out + c.y * p.o_st + h * p.o_sh) + 4 * x, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  }
+}
+
+template <typename TI, int D>
+hipError_t launch_step(const AttnParams& p, hipStream_t s) {
+  using H = StepShape<TI, D>;
+  hipLaunchKernelGGL((step_kernel<TI, D>), dim3(p.waves / H::NW), dim3(64 * H::NW), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((join_kernel<TI, D>), dim3(p.waves, std::min(p.group, kDecodeHeads)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// prompts, 64 queries a workgroup: 16 a wave, tiles of 32 keys shared
+
+template <typename TI, int D>
+struct TileShape {
+  static constexpr int TT = 2, TK = 32, NW = 4, ROWS = 64;
+  static constexpr int RB = D * (int)sizeof(TI), GR = RB / 16, TILE = TK * RB;
+  static constexpr int PIECES = TK * GR / 64 / NW;  // copies of a tile, a wave
+  static constexpr int entries = 4 * TILE, total = entries + NW * 2 * 256;
+  static_assert(PIECES >= 1 && total <= 163840, "LDS");
+};
+
+// Where a workgroup's queries lie: rows [row, row + n) of q, at the places
+// from `place` on of a sequence whose keys start at row `start` (without a
+// table).
+struct TileRows {
+  int seq, start, row, n, place;
+};
+
+// The tile `i` of a head's: of a packed batch sequence s has those from
+// floor(cu[s] / rows) + s on, as many as it fills and some over.
+__device__ __forceinline__ bool tile_rows(const AttnParams& p, int64_t i, int rows, TileRows& t) {
+  int at;
+  if (p.cu) {
+    int lo = 0, hi = p.n_seq - 1;
+    while (lo < hi) {
+      const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
+      if ((int64_t)attn_cu(p, mid) / rows + mid <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    t.seq = lo;
+    t.start = attn_cu(p, lo);
+    t.n = attn_cu(p, (int64_t)lo + 1) - t.start;
+    at = (int)min((i - ((int64_t)t.start / rows + lo)) * rows, (int64_t)p.t_total);
+  } else {
+    const int each = (p.seq_len + rows - 1) / rows;
+    t.seq = (int)(i / each);
+    t.start = t.seq * p.seq_len;
+    t.n = p.seq_len;
+    at = (int)(i - (int64_t)t.seq * each) * rows;
+  }
+  if (at < 0 || at >= t.n) return false;
+  t.row = t.start + at;
+  t.place = at;
+  if (p.table) t.place += min(max(p.lens[t.seq], 0), p.max_len) - t.n;
+  t.n = min(t.n - at, rows);
+  return true;
+}
+
+template <typename TI, int D, bool PAGED>
+__global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
+  using H = TileShape<TI, D>;
+  constexpr int TT = H::TT, TK = H::TK, RB = H::RB, GR = H::GR, P = H::PIECES;
+  __shared__ __attribute__((aligned(1024))) char smem[H::total];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t item = blockIdx.x / p.heads;
+  const int h = blockIdx.x - (int)item * p.heads, kh = h / p.group;
+  TileRows t;
+  if (!tile_rows(p, item, H::ROWS, t)) return;
+  const int lo = t.place, hi = t.place + t.n - 1;  // the queries' places
+  const int mine = wave * 16 + (lane & 15), place = lo + mine;
+  char* const out = mine < t.n ? (char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh : nullptr;
+  AttnCore<TI, D, TT> core;
+  core.reset();
+  core.load((const char*)p.q + (int64_t)(t.row + mine) * p.q_st + h * p.q_sh, mine < t.n, lane);
+
+  // key tiles: those of the sinks, then those from the window's start on
+  const int end = hi / TK + (hi >= 0 ? 1 : 0);
+  const int from = p.window > 0 ? max(0, max(lo, 0) - p.window + 1) / TK : 0;
+  const int sinks = p.window > 0 ? (min(p.sinks, hi + 1) + TK - 1) / TK : 0;
+  const auto after = [&](int k) { return k + 1 >= sinks && k + 1 < from ? from : k + 1; };
+  const uint32_t ring_at = attn_lds(smem), entries_at = attn_lds(smem + H::entries + wave * 512);
+  const int* entries = (const int*)(smem + H::entries + wave * 512);
+  const auto live = [&](int j) { return j <= hi && (p.window <= 0 || j > max(lo, 0) - p.window || j < p.sinks); };
+  const auto ask = [&](int k, int row) {
+    if (!PAGED) return;
+    const int j = k * TK + lane;
+    const void* a = p.lens;
+    if (k < end && lane < TK && live(j)) a = p.table + t.seq * p.table_st + attn_quotient(p.page, j);
+    attn_copy4(entries_at + row * 256, a);
+  };
+  const auto fetch = [&](int k, int row, int stage) -> uint32_t {
+    const int j = k * TK + lane;
+    bool there = k < end && lane < TK && live(j);
+    int page = 0, in = j;
+    if (PAGED && there) {
+      page = entries[row * 64 + lane];
+      there = (uint32_t)page < (uint32_t)p.pages;
+      in = j - attn_quotient(p.page, j) * (int)p.page.d;
+    }
+    if (!PAGED) in += t.start;
+    const uint32_t mask = (uint32_t)__ballot(there);
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      const char* base = kind ? (const char*)p.v + kh * p.v_sh : (const char*)p.k + kh * p.k_sh;
+      const int64_t sp = kind ? p.v_sp : p.k_sp, st = kind ? p.v_st : p.k_st;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int piece = i * H::NW + wave, r = piece * (64 / GR) + lane / GR;
+        const int pl = __shfl(in, r);
+        int64_t o = pl * st;
+        if (PAGED) o += __shfl(page, r) * sp;
+        const char* a = base + o + (((lane % GR) ^ ssm_swz<GR>(r)) * 16);
+        attn_copy16(ring_at + (2 * stage + kind) * H::TILE + piece * 1024,
+                    (mask >> r) & 1u ? a : (const char*)attn_zeros);
+      }
+    }
+    return mask;
+  };
+  int now = sinks > 0 ? 0 : from, then = after(now), later = after(then);
+  int stage = 0;
+  ask(now, 0);
+  attn_wait<0>();
+  uint32_t there = fetch(now, 0, 0), there_then;
+  ask(then, 1);
+  while (now < end) {
+    attn_wait_lds();
+    ask(later, stage);
+    attn_wait<PAGED ? 1 : 0>();
+    lds_barrier();
+    there_then = fetch(then, stage ^ 1, stage ^ 1);
+    f32x4 s[TT];
+    core.scores(smem + 2 * stage * H::TILE, s, lane);
+#pragma unroll
+    for (int k = 0; k < TT; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int in = 16 * k + 4 * (lane >> 4) + e, j = now * TK + in;
+        const bool see = ((there >> in) & 1u) && j <= place && (p.window <= 0 || place - j < p.window || j < p.sinks);
+        s[k][e] = see ? s[k][e] * p.scale : -INFINITY;
+      }
+    core.weigh(s);
+    core.add(smem + (2 * stage + 1) * H::TILE, s, lane);
+    now = then;
+    then = later;
+    later = after(later);
+    there = there_then;
+    stage ^= 1;
+  }
+  attn_wait<0>();  // no copy may land after the workgroup's end
+  core.store(out, lane);
+}
+
+template <typename TI, int D>
+hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
+  using H = TileShape<TI, D>;
+  const int64_t tiles = p.cu ? (int64_t)p.t_total / H::ROWS + p.n_seq
+                             : (int64_t)p.n_seq * ((p.seq_len + H::ROWS - 1) / H::ROWS);
+  const dim3 grid((unsigned)(tiles * p.heads)), threads(256);
+  if (p.table)
+    hipLaunchKernelGGL((tile_kernel<TI, D, true>), grid, threads, 0, s, p);
+  else
+    hipLaunchKernelGGL((tile_kernel<TI, D, false>), grid, threads, 0, s, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int attn_tile_rows(bool, int) { return 128; }
+int attn_tile_rows(bool, int) { return 64; }
 hipError_t launch_attn_prefill(bool bf16_in, int d, const AttnParams& p, hipStream_t s) {
-  return launch_plain<false>(bf16_in, d, p, s);
+  if (d == 64) return bf16_in ? launch_tiles<bf16, 64>(p, s) : launch_tiles<float, 64>(p, s);
+  if (d == 128) return bf16_in ? launch_tiles<bf16, 128>(p, s) : launch_tiles<float, 128>(p, s);
+  return bf16_in ? launch_tiles<bf16, 256>(p, s) : launch_tiles<float, 256>(p, s);
 }
 
-int attn_decode_waves(bool, int) { return 1024; }
+// One workgroup on each of 256 compute units.
+int attn_decode_waves(bool bf16_in, int d) {
+  return 256 * (bf16_in ? (d == 64 ? 8 : d == 128 ? 4 : 2) : (d == 64 ? 8 : d == 128 ? 4 : 2));
+}
 hipError_t launch_attn_decode(bool bf16_in, int d, const AttnParams& p, hipStream_t s) {
-  return launch_plain<true>(bf16_in, d, p, s);
+  if (d == 64) return bf16_in ? launch_step<bf16, 64>(p, s) : launch_step<float, 64>(p, s);
+  if (d == 128) return bf16_in ? launch_step<bf16, 128>(p, s) : launch_step<float, 128>(p, s);
+  return bf16_in ? launch_step<bf16, 256>(p, s) : launch_step<float, 256>(p, s);
 }
 
 }  // namespace gdn

@@ -20,7 +20,7 @@ namespace {
 
 constexpr int64_t kMaxThreads = (int64_t)1 << 32;  // of one launch
 constexpr size_t kAlign = 256;
-constexpr int64_t kMaxRequests = (int64_t)1 << 24;
+constexpr int64_t kMaxRequests = (int64_t)1 << 20;
 
 bool attn_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
@@ -189,7 +189,7 @@ void fill(const Attn& A, const gdn_tensor* q, const gdn_tensor* k, const gdn_ten
 size_t decode_workspace(bool bf16, int64_t d) {
   const size_t waves = (size_t)attn_decode_waves(bf16, (int)d);
   const size_t parts = (2 * waves * attn_part_floats((int)d) * 4 + kAlign - 1) / kAlign * kAlign;
-  return parts + (waves * 8 + kAlign - 1) / kAlign * kAlign;
+  return parts + (waves * 16 + kAlign - 1) / kAlign * kAlign;
 }
 
 }  // namespace
@@ -205,7 +205,7 @@ int gdn_cache_plan(const gdn_tensor* ctx_lens, const gdn_tensor* cu_seqlens, gdn
   int rc;
   if ((rc = check_ints(ctx_lens, "ctx_lens", -1))) return rc;
   const int64_t n = ctx_lens->shape[0];
-  if (n > kMaxRequests) return api_fail(GDN_ERR_SHAPE, "at most 2^24 requests");
+  if (n > kMaxRequests) return api_fail(GDN_ERR_SHAPE, "at most 2^20 requests");
   if ((rc = check_table(block_table, n)) || (rc = check_ints(free_pages, "free_pages", -1)) ||
       (rc = check_ints(n_free, "n_free", 1)) || (rc = check_ints(seq_lens, "seq_lens", n)) ||
       (rc = check_ints(slots, "slots", -1, GDN_DTYPE_I64)) || (rc = check_ints(n_free_out, "n_free_out", 1)) ||
@@ -258,7 +258,7 @@ int gdn_cache_release(const gdn_tensor* done, gdn_tensor* seq_lens, gdn_tensor* 
   int rc;
   if ((rc = check_ints(done, "done", -1))) return rc;
   const int64_t n = done->shape[0];
-  if (n > kMaxRequests) return api_fail(GDN_ERR_SHAPE, "at most 2^24 requests");
+  if (n > kMaxRequests) return api_fail(GDN_ERR_SHAPE, "at most 2^20 requests");
   if ((rc = check_table(block_table, n)) || (rc = check_ints(seq_lens, "seq_lens", n)) ||
       (rc = check_ints(free_pages, "free_pages", -1)) || (rc = check_ints(n_free, "n_free", 1)) ||
       (rc = check_page(page_size, block_table->shape[1])) || (rc = check_distinct(block_table, "block_table")))
@@ -437,7 +437,7 @@ int gdn_attn_decode(const gdn_tensor* q, const gdn_tensor* k_cache, const gdn_te
   A.T = n;
   A.H = q->shape[1];
   A.D = q->shape[2];
-  if (n > kMaxRequests) return api_fail(GDN_ERR_SHAPE, "at most 2^24 sequences");
+  if (n > kMaxRequests) return api_fail(GDN_ERR_SHAPE, "at most 2^20 sequences");
   if ((rc = parse_caches(k_cache, v_cache, block_table, seq_lens, n, &A)) ||
       (rc = check_heads(A, q, k_cache, v_cache, out)))
     return rc;
@@ -461,7 +461,7 @@ int gdn_attn_decode(const gdn_tensor* q, const gdn_tensor* k_cache, const gdn_te
   p.t_total = (int32_t)n;
   p.waves = attn_decode_waves(bf16, (int)A.D);
   p.parts = (float*)workspace;
-  p.chains = (int32_t*)((char*)workspace + need - ((size_t)p.waves * 8 + kAlign - 1) / kAlign * kAlign);
+  p.chains = (int32_t*)((char*)workspace + need - ((size_t)p.waves * 16 + kAlign - 1) / kAlign * kAlign);
   const hipError_t e = launch_attn_decode(bf16, (int)A.D, p, (hipStream_t)stream);
   if (e != hipSuccess) return api_fail(GDN_ERR_HIP, "attention launch: %s", hipGetErrorString(e));
   return GDN_OK;

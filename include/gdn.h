@@ -629,7 +629,7 @@ int gdn_add_rms_norm(const gdn_tensor* x, const gdn_tensor* residual, const floa
  * behind the pages that a request's length needs are not read.  A page
  * outside the cache, inside that length, holds no token that is seen; lengths
  * below 0 or past M * page_size count as those.  page_size is 1 or more,
- * M * page_size and the tokens at most 2^31 - 2^21, requests at most 2^24.
+ * M * page_size and the tokens at most 2^31 - 2^21, requests at most 2^20.
  */
 
 /*
