@@ -82,6 +82,47 @@ __device__ __forceinline__ void attn_wait_lds() {
   asm volatile("" ::: "memory");
 }
 
+// Granule g of row r of a tile sits at granule g ^ attn_swz(r), so that the
+// lanes that LDS serves together meet distinct banks: 16 rows of one granule
+// (keys as an operand), and four or eight rows of 64 or 32 bytes (values by
+// columns).  Rows of 128 bytes alternate between the halves of the banks.
+template <int GR>
+__device__ __forceinline__ int attn_swz(int r) {
+  const int low = ((r >> 1) & 2) | ((r >> 3) & 1);
+  return GR == 8 ? ((r & 2) << 1) | low : ((r & 3) << 2) | low;
+}
+
+// Columns of values: column 16 i + l % 16 over 16 or 32 keys (see ssm_tr).
+template <typename TI, int D>
+struct AttnCols {
+  static constexpr int RB = D * (int)sizeof(TI), GR = RB / 16;
+  uint32_t at[4];  // bf16: [0]; f32: one for each of four rows
+  __device__ __forceinline__ AttnCols(int lane) {
+    const int q = lane >> 4, j = lane & 15;
+    if constexpr (sizeof(TI) == 2) {
+      const int c = 4 * (j & 3), r = 4 * q + (j >> 2);
+      at[0] = r * RB + (((c >> 3) ^ attn_swz<GR>(r)) * 16) + (c & 4) * 2;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 4 * q + e;
+        at[e] = r * RB + (((j >> 2) ^ attn_swz<GR>(r)) * 16) + (j & 3) * 4;
+      }
+    }
+  }
+  __device__ __forceinline__ typename Unit<TI>::type column(const char* tile, int i, int t) const {
+    if constexpr (sizeof(TI) == 2) {
+      const char* a = tile + (at[0] ^ (i * 32)) + t * 32 * RB;
+      return ssm_tr(a, a + 16 * RB);
+    } else {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *(const float*)(tile + (at[e] ^ (i * 64)) + t * 16 * RB);
+      return v;
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------
 // 16 queries of a wave against tiles of 16 TT keys
 
@@ -113,7 +154,7 @@ struct AttnCore {
   // s[t][e]: key 16 t + 4 (l / 16) + e, query l % 16
   __device__ __forceinline__ void scores(const char* k, f32x4 (&s)[TT], int lane) const {
     const int r = lane & 15, g = lane >> 4;
-    const uint32_t at = r * RB + ((g ^ ssm_swz<GR>(r)) * 16);
+    const uint32_t at = r * RB + ((g ^ attn_swz<GR>(r)) * 16);
 #pragma unroll
     for (int t = 0; t < TT; ++t) s[t] = zero4();
 #pragma unroll
@@ -159,7 +200,7 @@ struct AttnCore {
   // O^T += V^T P^T; bf16 weights as two terms, hi and what it leaves, which
   // cost nothing where memory is waited for: within 2^-16 of the weight.
   __device__ __forceinline__ void add(const char* v, const f32x4 (&s)[TT], int lane) {
-    const SsmCols<TI, D> cols(0, lane);
+    const AttnCols<TI, D> cols(lane);
     if constexpr (S == 2) {
       static_assert(TT == 2, "two key tiles an operand unit");
       bf16x8 hi, lo;
@@ -354,7 +395,7 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
         for (int j = 0; j < P; ++j) {
           const int r = j * (64 / GR) + lane / GR;
           const int pg = __shfl(page, r), pl = __shfl(in, r);
-          const char* from = base + pg * sp + pl * st + (((lane % GR) ^ ssm_swz<GR>(r)) * 16);
+          const char* from = base + pg * sp + pl * st + (((lane % GR) ^ attn_swz<GR>(r)) * 16);
           attn_copy16(ring_at + (2 * stage + kind) * H::TILE + j * 1024, pg >= 0 ? from : (const char*)attn_zeros);
         }
       }
@@ -606,7 +647,7 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
         const int pl = __shfl(in, r);
         int64_t o = pl * st;
         if (PAGED) o += __shfl(page, r) * sp;
-        const char* a = base + o + (((lane % GR) ^ ssm_swz<GR>(r)) * 16);
+        const char* a = base + o + (((lane % GR) ^ attn_swz<GR>(r)) * 16);
         attn_copy16(ring_at + (2 * stage + kind) * H::TILE + piece * 1024,
                     (mask >> r) & 1u ? a : (const char*)attn_zeros);
       }
@@ -647,12 +688,224 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
   core.store(out, lane);
 }
 
+// ---------------------------------------------------------------------------
+// prompts, bf16: 32 queries a wave, tiles of 64 keys shared by four waves
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int D>
+struct PromptShape {
+  static constexpr int NW = 4, ROWS = 32 * NW, TK = 64;
+  static constexpr int RB = D * 2, GR = RB / 16, TILE = TK * RB;
+  static constexpr int P = TK * GR / 64 / NW;  // copies of a tile, a wave
+  static constexpr int entries = 4 * TILE, total = entries + NW * 2 * 256;
+};
+
+__device__ __forceinline__ void settle16(f32x16& a) { asm volatile("" : "+v"(a)); }
+
+template <int D, bool PAGED>
+__global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnParams p, int tiles) {
+  using H = PromptShape<D>;
+  constexpr int TK = H::TK, RB = H::RB, GR = H::GR, P = H::P, NS = D / 16, NC = D / 32;
+  __shared__ __attribute__((aligned(1024))) char smem[H::total];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int half = lane >> 5, col = lane & 31;
+  const int rank = blockIdx.x / p.heads, hp = blockIdx.x - rank * p.heads;
+  const int h = p.heads % 8 == 0 ? (hp & 7) * (p.heads / 8) + (hp >> 3) : hp, kh = h / p.group;
+  TileRows t;
+  if (!tile_rows(p, tiles - 1 - rank, H::ROWS, t)) return;
+  const int lo = t.place, hi = t.place + t.n - 1;
+  const int mine = wave * 32 + col, place = lo + mine;
+  const int wave_lo = lo + wave * 32, wave_hi = min(wave_lo + 31, hi);
+
+  bf16x8 q[NS];
+#pragma unroll
+  for (int u = 0; u < NS; ++u) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (mine < t.n) v = ld16((const char*)p.q + (int64_t)(t.row + mine) * p.q_st + h * p.q_sh + (2 * u + half) * 16);
+    q[u] = __builtin_bit_cast(bf16x8, v);
+  }
+  f32x16 o[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
+  float m = -INFINITY, l = 0.f;
+
+  const int end = hi / TK + (hi >= 0 ? 1 : 0);
+  const int from = p.window > 0 ? max(0, max(lo, 0) - p.window + 1) / TK : 0;
+  const int sinks = p.window > 0 ? (min(p.sinks, hi + 1) + TK - 1) / TK : 0;
+  const auto after = [&](int k) { return k + 1 >= sinks && k + 1 < from ? from : k + 1; };
+  const uint32_t ring_at = attn_lds(smem), entries_at = attn_lds(smem + H::entries + wave * 512);
+  const int* entries = (const int*)(smem + H::entries + wave * 512);
+  const int low = p.window > 0 ? max(lo, 0) - p.window : -1;  // the last key before every window
+  const auto live = [&](int j) { return j <= hi && (j > low || j < p.sinks); };
+  const auto ask = [&](int k, int row) {
+    if (!PAGED) return;
+    const int j = k * TK + lane;
+    const void* a = p.lens;
+    if (k < end && live(j)) a = p.table + t.seq * p.table_st + attn_quotient(p.page, j);
+    attn_copy4(entries_at + row * 256, a);
+  };
+  const char* const k_base = (const char*)p.k + kh * p.k_sh;
+  const char* const v_base = (const char*)p.v + kh * p.v_sh;
+  const auto fetch = [&](int k, int row, int stage) -> uint64_t {
+    const int j = k * TK + lane;
+    bool there = k < end && live(j);
+    int64_t ko, vo;
+    if (PAGED) {
+      const int page = entries[row * 64 + lane];
+      there = there && (uint32_t)page < (uint32_t)p.pages;
+      const int in = j - attn_quotient(p.page, j) * (int)p.page.d;
+      ko = page * p.k_sp + in * p.k_st;
+      vo = page * p.v_sp + in * p.v_st;
+    } else {
+      ko = (int64_t)(t.start + j) * p.k_st;
+      vo = (int64_t)(t.start + j) * p.v_st;
+    }
+    const uint64_t mask = __ballot(there);
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int piece = i * H::NW + wave, r = piece * (64 / GR) + lane / GR;
+        const int64_t off = __shfl(kind ? vo : ko, r);
+        const char* a = (kind ? v_base : k_base) + off + (((lane % GR) ^ attn_swz<GR>(r)) * 16);
+        attn_copy16(ring_at + (2 * stage + kind) * H::TILE + piece * 1024,
+                    (mask >> r) & 1u ? a : (const char*)attn_zeros);
+      }
+    }
+    return mask;
+  };
+
+  // operand places: keys by rows, values by columns (two halves of 16 keys)
+  const uint32_t k_at = col * RB + ((half ^ attn_swz<GR>(col)) * 16);
+  const int vr = 4 * half + ((lane & 15) >> 2), vc = (lane & 16) + 4 * (lane & 3);
+  const uint32_t v_at0 = vr * RB + (((vc >> 3) ^ attn_swz<GR>(vr)) * 16) + (vc & 4) * 2;
+  const uint32_t v_at1 = (vr + 8) * RB + (((vc >> 3) ^ attn_swz<GR>(vr + 8)) * 16) + (vc & 4) * 2;
+
+  int now = sinks > 0 ? 0 : from, then = after(now), later = after(then);
+  int stage = 0;
+  ask(now, 0);
+  attn_wait<0>();
+  uint64_t there = fetch(now, 0, 0), there_then;
+  ask(then, 1);
+  while (now < end) {
+    attn_wait_lds();
+    ask(later, stage);
+    attn_wait<PAGED ? 1 : 0>();
+    lds_barrier();
+    there_then = fetch(then, stage ^ 1, stage ^ 1);
+    const int j0 = now * TK;
+    const bool any = wave_lo <= hi && j0 <= wave_hi &&
+                     (p.window <= 0 || j0 + TK - 1 > max(wave_lo, 0) - p.window || j0 < p.sinks);
+    if (any) {
+      const char* kt = smem + 2 * stage * H::TILE;
+      const char* vt = kt + H::TILE;
+      f32x16 s[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const bf16x8 a = *(const bf16x8*)(kt + (k_at ^ (u * 32)) + b * 32 * RB);
+          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[u], s[b], 0, 0, 0);
+        }
+      settle16(s[0]);
+      settle16(s[1]);
+      const bool whole = j0 + TK - 1 <= wave_lo && there == ~0ull &&
+                         (p.window <= 0 || j0 > wave_hi - p.window || j0 + TK <= p.sinks);
+      if (!whole) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int in = 32 * b + 8 * (e >> 2) + 4 * half + (e & 3), j = j0 + in;
+            const bool see = ((there >> in) & 1u) && j <= place && (p.window <= 0 || place - j < p.window || j < p.sinks);
+            s[b][e] = see ? s[b][e] : -INFINITY;
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
+      top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
+      // O and l are rescaled only where the maximum has grown by more than
+      // 2^8: weights of up to 2^8 lose nothing in fp32 or bf16
+      if (__any(top > m + 8.f)) {
+        const float next = fmaxf(m, top);
+        const float keep = __builtin_amdgcn_exp2f(m - (next == -INFINITY ? 0.f : next));
+        m = next;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[i][e] *= keep;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+      bf16x8 w[4];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float x = __builtin_amdgcn_exp2f(s[b][e] * p.scale - base);
+          sum += x;
+          w[2 * b + (e >> 3)][e & 7] = (bf16)x;
+        }
+      l += sum;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const bf16x8 a = ssm_tr(vt + (v_at0 ^ (i * 64)) + u * 16 * RB, vt + (v_at1 ^ (i * 64)) + u * 16 * RB);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w[u], o[i], 0, 0, 0);
+        }
+#pragma unroll
+      for (int i = 0; i < NC; ++i) settle16(o[i]);
+    }
+    now = then;
+    then = later;
+    later = after(later);
+    there = there_then;
+    stage ^= 1;
+  }
+  attn_wait<0>();  // no copy may land after the workgroup's end
+  l += __shfl_xor(l, 32);
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  if (mine < t.n) {
+    bf16* out = (bf16*)((char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh) + 4 * half;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        store4<bf16>(out + 32 * i + 8 * j, o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
+                     o[i][4 * j + 3] * inv);
+  }
+}
+
+int64_t tiles_of(const AttnParams& p, int rows) {
+  return p.cu ? (int64_t)p.t_total / rows + p.n_seq : (int64_t)p.n_seq * ((p.seq_len + rows - 1) / rows);
+}
+
+template <int D>
+hipError_t launch_prompt(const AttnParams& p, hipStream_t s) {
+  const int64_t tiles = tiles_of(p, PromptShape<D>::ROWS);
+  const dim3 grid((unsigned)(tiles * p.heads)), threads(256);
+  if (p.table)
+    hipLaunchKernelGGL((prompt_kernel<D, true>), grid, threads, 0, s, p, (int)tiles);
+  else
+    hipLaunchKernelGGL((prompt_kernel<D, false>), grid, threads, 0, s, p, (int)tiles);
+  return hipGetLastError();
+}
+
 template <typename TI, int D>
 hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
-  using H = TileShape<TI, D>;
-  const int64_t tiles = p.cu ? (int64_t)p.t_total / H::ROWS + p.n_seq
-                             : (int64_t)p.n_seq * ((p.seq_len + H::ROWS - 1) / H::ROWS);
-  const dim3 grid((unsigned)(tiles * p.heads)), threads(256);
+  const dim3 grid((unsigned)(tiles_of(p, TileShape<TI, D>::ROWS) * p.heads)), threads(256);
   if (p.table)
     hipLaunchKernelGGL((tile_kernel<TI, D, true>), grid, threads, 0, s, p);
   else
@@ -662,11 +915,11 @@ hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
 
 }  // namespace
 
-int attn_tile_rows(bool, int) { return 64; }
+int attn_tile_rows(bool bf16_in, int) { return bf16_in ? 128 : 64; }
 hipError_t launch_attn_prefill(bool bf16_in, int d, const AttnParams& p, hipStream_t s) {
-  if (d == 64) return bf16_in ? launch_tiles<bf16, 64>(p, s) : launch_tiles<float, 64>(p, s);
-  if (d == 128) return bf16_in ? launch_tiles<bf16, 128>(p, s) : launch_tiles<float, 128>(p, s);
-  return bf16_in ? launch_tiles<bf16, 256>(p, s) : launch_tiles<float, 256>(p, s);
+  if (d == 64) return bf16_in ? launch_prompt<64>(p, s) : launch_tiles<float, 64>(p, s);
+  if (d == 128) return bf16_in ? launch_prompt<128>(p, s) : launch_tiles<float, 128>(p, s);
+  return bf16_in ? launch_prompt<256>(p, s) : launch_tiles<float, 256>(p, s);
 }
 
 // One workgroup on each of 256 compute units.
