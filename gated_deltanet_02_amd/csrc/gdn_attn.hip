@@ -63,6 +63,14 @@ __device__ __forceinline__ void attn_copy4(uint32_t lds, const void* from) {
                : "memory", "m0");
 }
 
+// The same from a common address and a lane's offset to it.
+__device__ __forceinline__ void attn_copy16(uint32_t lds, const void* base, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"((uint64_t)(uintptr_t)base)
+               : "memory", "m0");
+}
+
 __device__ __forceinline__ uint32_t attn_lds(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
@@ -701,6 +709,11 @@ struct PromptShape {
   static constexpr int entries = 4 * TILE, total = entries + NW * 2 * 256;
 };
 
+// The n lowest bits.
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : ((uint64_t)1 << n) - 1;
+}
+
 __device__ __forceinline__ void settle16(f32x16& a) { asm volatile("" : "+v"(a)); }
 
 template <int D, bool PAGED>
@@ -710,7 +723,11 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
   __shared__ __attribute__((aligned(1024))) char smem[H::total];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int half = lane >> 5, col = lane & 31;
-  const int rank = blockIdx.x / p.heads, hp = blockIdx.x - rank * p.heads;
+  int rank = blockIdx.x / p.heads;
+  const int hp = blockIdx.x - rank * p.heads;
+  // Long tiles first.  Where the chip holds all of them at once, two a compute
+  // unit, the second half the other way round.
+  if (gridDim.x <= 512 && 2 * rank >= tiles) rank = (tiles + 1) / 2 + tiles - 1 - rank;
   const int h = p.heads % 8 == 0 ? (hp & 7) * (p.heads / 8) + (hp >> 3) : hp, kh = h / p.group;
   TileRows t;
   if (!tile_rows(p, tiles - 1 - rank, H::ROWS, t)) return;
@@ -749,13 +766,49 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
   };
   const char* const k_base = (const char*)p.k + kh * p.k_sh;
   const char* const v_base = (const char*)p.v + kh * p.v_sh;
+  // A tile that is there as a whole is copied from common addresses, one a
+  // piece of PR rows (which pages of a multiple of PR keep together), and
+  // lanes' offsets that stay; others row by row.
+  constexpr int PR = 64 / GR;
+  const bool even = !PAGED || p.page.d % PR == 0;
+  uint32_t k_off[P], v_off[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int r = (i * H::NW + wave) * PR + lane / GR, row = PAGED ? lane / GR : r;
+    const uint32_t g = ((lane % GR) ^ attn_swz<GR>(r)) * 16;
+    k_off[i] = (uint32_t)row * (uint32_t)p.k_st + g;
+    v_off[i] = (uint32_t)row * (uint32_t)p.v_st + g;
+  }
   const auto fetch = [&](int k, int row, int stage) -> uint64_t {
     const int j = k * TK + lane;
     bool there = k < end && live(j);
+    int page = 0;
+    if (PAGED) {
+      page = entries[row * 64 + lane];
+      there = there && (uint32_t)page < (uint32_t)p.pages;
+    }
+    const uint64_t mask = __ballot(there);
+    const uint32_t to = ring_at + 2 * stage * H::TILE + wave * 1024;
+    if (mask == ~0ull && even) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        int64_t ko, vo;
+        if (PAGED) {
+          const int r = (i * H::NW + wave) * PR, at = k * TK + r;
+          const int pg = __builtin_amdgcn_readlane(page, r), in = at - attn_quotient(p.page, at) * (int)p.page.d;
+          ko = pg * p.k_sp + in * p.k_st;
+          vo = pg * p.v_sp + in * p.v_st;
+        } else {
+          ko = (int64_t)(t.start + k * TK) * p.k_st;
+          vo = (int64_t)(t.start + k * TK) * p.v_st;
+        }
+        attn_copy16(to + i * H::NW * 1024, k_base + ko, k_off[i]);
+        attn_copy16(to + i * H::NW * 1024 + H::TILE, v_base + vo, v_off[i]);
+      }
+      return mask;
+    }
     int64_t ko, vo;
     if (PAGED) {
-      const int page = entries[row * 64 + lane];
-      there = there && (uint32_t)page < (uint32_t)p.pages;
       const int in = j - attn_quotient(p.page, j) * (int)p.page.d;
       ko = page * p.k_sp + in * p.k_st;
       vo = page * p.v_sp + in * p.v_st;
@@ -763,17 +816,14 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
       ko = (int64_t)(t.start + j) * p.k_st;
       vo = (int64_t)(t.start + j) * p.v_st;
     }
-    const uint64_t mask = __ballot(there);
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int piece = i * H::NW + wave, r = piece * (64 / GR) + lane / GR;
-        const int64_t off = __shfl(kind ? vo : ko, r);
-        const char* a = (kind ? v_base : k_base) + off + (((lane % GR) ^ attn_swz<GR>(r)) * 16);
-        attn_copy16(ring_at + (2 * stage + kind) * H::TILE + piece * 1024,
-                    (mask >> r) & 1u ? a : (const char*)attn_zeros);
-      }
+    for (int i = 0; i < P; ++i) {
+      const int r = (i * H::NW + wave) * PR + lane / GR;
+      const int64_t kr = __shfl(ko, r), vr = __shfl(vo, r);
+      const int g = ((lane % GR) ^ attn_swz<GR>(r)) * 16;
+      const bool is = (mask >> r) & 1u;
+      attn_copy16(to + i * H::NW * 1024, is ? k_base + kr + g : (const char*)attn_zeros);
+      attn_copy16(to + i * H::NW * 1024 + H::TILE, is ? v_base + vr + g : (const char*)attn_zeros);
     }
     return mask;
   };
@@ -786,10 +836,16 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
 
   int now = sinks > 0 ? 0 : from, then = after(now), later = after(then);
   int stage = 0;
-  ask(now, 0);
-  attn_wait<0>();
+  if (PAGED) {
+    ask(now, 0);
+    attn_wait<0>();
+  }
   uint64_t there = fetch(now, 0, 0), there_then;
   ask(then, 1);
+  f32x16 none;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) none[e] = 0.f;
+  settle16(none);
   while (now < end) {
     attn_wait_lds();
     ask(later, stage);
@@ -804,29 +860,26 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
       const char* vt = kt + H::TILE;
       f32x16 s[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
-#pragma unroll
       for (int u = 0; u < NS; ++u)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const bf16x8 a = *(const bf16x8*)(kt + (k_at ^ (u * 32)) + b * 32 * RB);
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[u], s[b], 0, 0, 0);
+          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[u], u == 0 ? none : s[b], 0, 0, 0);
         }
       settle16(s[0]);
       settle16(s[1]);
       const bool whole = j0 + TK - 1 <= wave_lo && there == ~0ull &&
                          (p.window <= 0 || j0 > wave_hi - p.window || j0 + TK <= p.sinks);
       if (!whole) {
+        // the keys that the lane's query sees, a bit each
+        uint64_t see = there & low_bits(place - j0 + 1);
+        if (p.window > 0) see &= ~low_bits(place - j0 - p.window + 1) | low_bits(p.sinks - j0);
+        see >>= 4 * half;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int in = 32 * b + 8 * (e >> 2) + 4 * half + (e & 3), j = j0 + in;
-            const bool see = ((there >> in) & 1u) && j <= place && (p.window <= 0 || place - j < p.window || j < p.sinks);
-            s[b][e] = see ? s[b][e] : -INFINITY;
-          }
+          for (int e = 0; e < 16; ++e)
+            s[b][e] = ((uint32_t)(see >> (32 * b)) >> (8 * (e >> 2) + (e & 3))) & 1u ? s[b][e] : -INFINITY;
       }
       float top = s[0][0];
 #pragma unroll
