@@ -859,15 +859,32 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
       const char* kt = smem + 2 * stage * H::TILE;
       const char* vt = kt + H::TILE;
       f32x16 s[2];
+      bf16x8 a[2][NS];
 #pragma unroll
       for (int u = 0; u < NS; ++u)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const bf16x8 a = *(const bf16x8*)(kt + (k_at ^ (u * 32)) + b * 32 * RB);
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[u], u == 0 ? none : s[b], 0, 0, 0);
-        }
+        for (int b = 0; b < 2; ++b) a[b][u] = *(const bf16x8*)(kt + (k_at ^ (u * 32)) + b * 32 * RB);
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[b][u], q[u], u == 0 ? none : s[b], 0, 0, 0);
+      // eight operands on their way ahead of the products
+      __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+      for (int u = 0; u < NS - 4; ++u) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
       settle16(s[0]);
       settle16(s[1]);
+      const auto value = [&](int u, int i) {
+        return ssm_tr(vt + (v_at0 ^ (i * 64)) + u * 16 * RB, vt + (v_at1 ^ (i * 64)) + u * 16 * RB);
+      };
+      bf16x8 first[NC];  // the first of V's operands, asked for early
+#pragma unroll
+      for (int i = 0; i < NC; ++i) first[i] = value(0, i);
       const bool whole = j0 + TK - 1 <= wave_lo && there == ~0ull &&
                          (p.window <= 0 || j0 > wave_hi - p.window || j0 + TK <= p.sinks);
       if (!whole) {
@@ -915,8 +932,7 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-          const bf16x8 a = ssm_tr(vt + (v_at0 ^ (i * 64)) + u * 16 * RB, vt + (v_at1 ^ (i * 64)) + u * 16 * RB);
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w[u], o[i], 0, 0, 0);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u == 0 ? first[i] : value(u, i), w[u], o[i], 0, 0, 0);
         }
 #pragma unroll
       for (int i = 0; i < NC; ++i) settle16(o[i]);
