@@ -714,6 +714,12 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : ((uint64_t)1 << n) - 1;
 }
 
+// The larger of a lane's value and of the one 32 lanes away.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 __device__ __forceinline__ void settle16(f32x16& a) { asm volatile("" : "+v"(a)); }
 
 template <int D, bool PAGED>
@@ -779,39 +785,53 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
     k_off[i] = (uint32_t)row * (uint32_t)p.k_st + g;
     v_off[i] = (uint32_t)row * (uint32_t)p.v_st + g;
   }
-  const auto fetch = [&](int k, int row, int stage) -> uint64_t {
-    const int j = k * TK + lane;
-    bool there = k < end && live(j);
-    int page = 0;
+  // Where a tile's rows lie: the lane's key's page, and which keys there are.
+  struct Where {
+    int tile, page;
+    uint64_t there;
+  };
+  const auto look = [&](int k, int row) {
+    Where w{k, 0, 0};
+    const int j0 = k * TK, j = j0 + lane;
+    if (!PAGED && j0 + TK - 1 <= hi && (j0 > low || j0 + TK <= p.sinks)) {
+      w.there = ~0ull;
+      return w;
+    }
+    bool is = k < end && live(j);
     if (PAGED) {
-      page = entries[row * 64 + lane];
-      there = there && (uint32_t)page < (uint32_t)p.pages;
+      w.page = entries[row * 64 + lane];
+      is = is && (uint32_t)w.page < (uint32_t)p.pages;
     }
-    const uint64_t mask = __ballot(there);
-    const uint32_t to = ring_at + 2 * stage * H::TILE + wave * 1024;
-    if (mask == ~0ull && even) {
+    w.there = __ballot(is);
+    return w;
+  };
+  // Piece i of a tile that is there as a whole: keys, then values.
+  const auto copy = [&](const Where& w, uint32_t to, int i) {
+    int64_t ko, vo;
+    if (PAGED) {
+      const int r = (i * H::NW + wave) * PR, at = w.tile * TK + r;
+      const int pg = __builtin_amdgcn_readlane(w.page, r), in = at - attn_quotient(p.page, at) * (int)p.page.d;
+      ko = pg * p.k_sp + in * p.k_st;
+      vo = pg * p.v_sp + in * p.v_st;
+    } else {
+      ko = (int64_t)(t.start + w.tile * TK) * p.k_st;
+      vo = (int64_t)(t.start + w.tile * TK) * p.v_st;
+    }
+    attn_copy16(to + i * H::NW * 1024, k_base + ko, k_off[i]);
+    attn_copy16(to + i * H::NW * 1024 + H::TILE, v_base + vo, v_off[i]);
+  };
+  const auto fetch = [&](const Where& w, uint32_t to) {
+    if (w.there == ~0ull && even) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        int64_t ko, vo;
-        if (PAGED) {
-          const int r = (i * H::NW + wave) * PR, at = k * TK + r;
-          const int pg = __builtin_amdgcn_readlane(page, r), in = at - attn_quotient(p.page, at) * (int)p.page.d;
-          ko = pg * p.k_sp + in * p.k_st;
-          vo = pg * p.v_sp + in * p.v_st;
-        } else {
-          ko = (int64_t)(t.start + k * TK) * p.k_st;
-          vo = (int64_t)(t.start + k * TK) * p.v_st;
-        }
-        attn_copy16(to + i * H::NW * 1024, k_base + ko, k_off[i]);
-        attn_copy16(to + i * H::NW * 1024 + H::TILE, v_base + vo, v_off[i]);
-      }
-      return mask;
+      for (int i = 0; i < P; ++i) copy(w, to, i);
+      return;
     }
+    const int j = w.tile * TK + lane;
     int64_t ko, vo;
     if (PAGED) {
       const int in = j - attn_quotient(p.page, j) * (int)p.page.d;
-      ko = page * p.k_sp + in * p.k_st;
-      vo = page * p.v_sp + in * p.v_st;
+      ko = w.page * p.k_sp + in * p.k_st;
+      vo = w.page * p.v_sp + in * p.v_st;
     } else {
       ko = (int64_t)(t.start + j) * p.k_st;
       vo = (int64_t)(t.start + j) * p.v_st;
@@ -821,12 +841,12 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
       const int r = (i * H::NW + wave) * PR + lane / GR;
       const int64_t kr = __shfl(ko, r), vr = __shfl(vo, r);
       const int g = ((lane % GR) ^ attn_swz<GR>(r)) * 16;
-      const bool is = (mask >> r) & 1u;
+      const bool is = (w.there >> r) & 1u;
       attn_copy16(to + i * H::NW * 1024, is ? k_base + kr + g : (const char*)attn_zeros);
       attn_copy16(to + i * H::NW * 1024 + H::TILE, is ? v_base + vr + g : (const char*)attn_zeros);
     }
-    return mask;
   };
+  const auto stage_at = [&](int stage) { return ring_at + 2 * stage * H::TILE + wave * 1024; };
 
   // operand places: keys by rows, values by columns (two halves of 16 keys)
   const uint32_t k_at = col * RB + ((half ^ attn_swz<GR>(col)) * 16);
@@ -840,7 +860,8 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
     ask(now, 0);
     attn_wait<0>();
   }
-  uint64_t there = fetch(now, 0, 0), there_then;
+  Where here = look(now, 0);
+  fetch(here, stage_at(0));
   ask(then, 1);
   f32x16 none;
 #pragma unroll
@@ -851,32 +872,35 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
     ask(later, stage);
     attn_wait<PAGED ? 1 : 0>();
     lds_barrier();
-    there_then = fetch(then, stage ^ 1, stage ^ 1);
+    const Where next = look(then, stage ^ 1);
     const int j0 = now * TK;
     const bool any = wave_lo <= hi && j0 <= wave_hi &&
                      (p.window <= 0 || j0 + TK - 1 > max(wave_lo, 0) - p.window || j0 < p.sinks);
+    // the next tile's copies run between this one's products: one after the
+    // other they would wait for the way into LDS
+    const bool between = any && next.there == ~0ull && even;
+    if (!between) fetch(next, stage_at(stage ^ 1));
     if (any) {
       const char* kt = smem + 2 * stage * H::TILE;
       const char* vt = kt + H::TILE;
       f32x16 s[2];
-      bf16x8 a[2][NS];
+      bf16x8 a[NS][2];
+      const auto key = [&](int u, int b) { return *(const bf16x8*)(kt + (k_at ^ (u * 32)) + b * 32 * RB); };
+      constexpr int AHEAD = 4, EVERY = NS / P;  // operands on their way; products to a copy
 #pragma unroll
-      for (int u = 0; u < NS; ++u)
+      for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) a[b][u] = *(const bf16x8*)(kt + (k_at ^ (u * 32)) + b * 32 * RB);
+        for (int b = 0; b < 2; ++b) a[u][b] = key(u, b);
 #pragma unroll
-      for (int u = 0; u < NS; ++u)
+      for (int u = 0; u < NS; ++u) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[b][u], q[u], u == 0 ? none : s[b], 0, 0, 0);
-      // eight operands on their way ahead of the products
-      __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
-#pragma unroll
-      for (int u = 0; u < NS - 4; ++u) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        for (int b = 0; b < 2; ++b) {
+          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[u][b], q[u], u == 0 ? none : s[b], 0, 0, 0);
+          if (u + AHEAD < NS) a[u + AHEAD][b] = key(u + AHEAD, b);
+        }
+        if (u % EVERY == 0 && between) copy(next, stage_at(stage ^ 1), u / EVERY);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
       settle16(s[0]);
       settle16(s[1]);
       const auto value = [&](int u, int i) {
@@ -885,11 +909,11 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
       bf16x8 first[NC];  // the first of V's operands, asked for early
 #pragma unroll
       for (int i = 0; i < NC; ++i) first[i] = value(0, i);
-      const bool whole = j0 + TK - 1 <= wave_lo && there == ~0ull &&
+      const bool whole = j0 + TK - 1 <= wave_lo && here.there == ~0ull &&
                          (p.window <= 0 || j0 > wave_hi - p.window || j0 + TK <= p.sinks);
       if (!whole) {
         // the keys that the lane's query sees, a bit each
-        uint64_t see = there & low_bits(place - j0 + 1);
+        uint64_t see = here.there & low_bits(place - j0 + 1);
         if (p.window > 0) see &= ~low_bits(place - j0 - p.window + 1) | low_bits(p.sinks - j0);
         see >>= 4 * half;
 #pragma unroll
@@ -903,7 +927,7 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
-      top = fmaxf(top, __shfl_xor(top, 32)) * p.scale;
+      top = max_halves(top) * p.scale;
       // O and l are rescaled only where the maximum has grown by more than
       // 2^8: weights of up to 2^8 lose nothing in fp32 or bf16
       if (__any(top > m + 8.f)) {
@@ -940,7 +964,7 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
     now = then;
     then = later;
     later = after(later);
-    there = there_then;
+    here = next;
     stage ^= 1;
   }
   attn_wait<0>();  // no copy may land after the workgroup's end
