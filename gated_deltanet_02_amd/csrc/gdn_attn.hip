@@ -701,13 +701,18 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-template <int D>
+template <int D, int GROUPS>
 struct PromptShape {
-  static constexpr int NW = 4, ROWS = 32 * NW, TK = 64;
+  static constexpr int NW = 4, ROWS = 32 * NW, TK = 64;  // NW: waves of a group
   static constexpr int RB = D * 2, GR = RB / 16, TILE = TK * RB;
-  static constexpr int P = TK * GR / 64 / NW;  // copies of a tile, a wave
-  static constexpr int entries = 4 * TILE, total = entries + NW * 2 * 256;
+  static constexpr int P = TK * GR / 64 / NW;  // copies of a tile's keys, a wave
+  static constexpr int ring = 4 * TILE, entries = GROUPS * ring, total = entries + GROUPS * NW * 2 * 256;
+  // the join: of every wave half of O, and m and l
+  static constexpr int box = 64 * D, join = 2 * NW * (box + 512);
+  static_assert(total <= 163840 && (GROUPS == 1 || join <= total), "LDS");
 };
+
+constexpr int kPromptRows = PromptShape<64, 1>::ROWS;
 
 // The n lowest bits.
 __device__ __forceinline__ uint64_t low_bits(int n) {
@@ -722,18 +727,19 @@ __device__ __forceinline__ float max_halves(float x) {
 
 __device__ __forceinline__ void settle16(f32x16& a) { asm volatile("" : "+v"(a)); }
 
-template <int D, bool PAGED>
-__global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnParams p, int tiles) {
-  using H = PromptShape<D>;
+template <int D, bool PAGED, int GROUPS>
+__global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kernel(AttnParams p, int tiles) {
+  using H = PromptShape<D, GROUPS>;
   constexpr int TK = H::TK, RB = H::RB, GR = H::GR, P = H::P, NS = D / 16, NC = D / 32;
   __shared__ __attribute__((aligned(1024))) char smem[H::total];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int group = wid >> 2, wave = wid & 3;
   const int half = lane >> 5, col = lane & 31;
   int rank = blockIdx.x / p.heads;
   const int hp = blockIdx.x - rank * p.heads;
   // Long tiles first.  Where the chip holds all of them at once, two a compute
   // unit, the second half the other way round.
-  if (gridDim.x <= 512 && 2 * rank >= tiles) rank = (tiles + 1) / 2 + tiles - 1 - rank;
+  if (GROUPS == 1 && gridDim.x <= 512 && 2 * rank >= tiles) rank = (tiles + 1) / 2 + tiles - 1 - rank;
   const int h = p.heads % 8 == 0 ? (hp & 7) * (p.heads / 8) + (hp >> 3) : hp, kh = h / p.group;
   TileRows t;
   if (!tile_rows(p, tiles - 1 - rank, H::ROWS, t)) return;
@@ -755,12 +761,19 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
     for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
   float m = -INFINITY, l = 0.f;
 
+  // key tiles: those of the sinks, then those from the window's start on; a
+  // group's are every GROUPS-th
   const int end = hi / TK + (hi >= 0 ? 1 : 0);
   const int from = p.window > 0 ? max(0, max(lo, 0) - p.window + 1) / TK : 0;
-  const int sinks = p.window > 0 ? (min(p.sinks, hi + 1) + TK - 1) / TK : 0;
-  const auto after = [&](int k) { return k + 1 >= sinks && k + 1 < from ? from : k + 1; };
-  const uint32_t ring_at = attn_lds(smem), entries_at = attn_lds(smem + H::entries + wave * 512);
-  const int* entries = (const int*)(smem + H::entries + wave * 512);
+  const int sinks = p.window > 0 ? min((min(p.sinks, hi + 1) + TK - 1) / TK, from) : 0;
+  const int turns = (max(0, sinks + end - from) + GROUPS - 1) / GROUPS;
+  const auto tile_at = [&](int j) {  // the group's tile j; `end` or more: none
+    const int i = GROUPS * j + group;
+    return i < sinks ? i : from + i - sinks;
+  };
+  const char* const ring = smem + group * H::ring;
+  const uint32_t ring_at = attn_lds(ring), entries_at = attn_lds(smem + H::entries + wid * 512);
+  const int* entries = (const int*)(smem + H::entries + wid * 512);
   const int low = p.window > 0 ? max(lo, 0) - p.window : -1;  // the last key before every window
   const auto live = [&](int j) { return j <= hi && (j > low || j < p.sinks); };
   const auto ask = [&](int k, int row) {
@@ -854,34 +867,33 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
   const uint32_t v_at0 = vr * RB + (((vc >> 3) ^ attn_swz<GR>(vr)) * 16) + (vc & 4) * 2;
   const uint32_t v_at1 = (vr + 8) * RB + (((vc >> 3) ^ attn_swz<GR>(vr + 8)) * 16) + (vc & 4) * 2;
 
-  int now = sinks > 0 ? 0 : from, then = after(now), later = after(then);
-  int stage = 0;
   if (PAGED) {
-    ask(now, 0);
+    ask(tile_at(0), 0);
     attn_wait<0>();
   }
-  Where here = look(now, 0);
+  Where here = look(tile_at(0), 0);
   fetch(here, stage_at(0));
-  ask(then, 1);
+  ask(tile_at(1), 1);
   f32x16 none;
 #pragma unroll
   for (int e = 0; e < 16; ++e) none[e] = 0.f;
   settle16(none);
-  while (now < end) {
+  for (int j = 0; j < turns; ++j) {
+    const int stage = j & 1;
     attn_wait_lds();
-    ask(later, stage);
+    ask(tile_at(j + 2), stage);
     attn_wait<PAGED ? 1 : 0>();
     lds_barrier();
-    const Where next = look(then, stage ^ 1);
-    const int j0 = now * TK;
-    const bool any = wave_lo <= hi && j0 <= wave_hi &&
+    const Where next = look(tile_at(j + 1), stage ^ 1);
+    const int j0 = here.tile * TK;
+    const bool any = here.tile < end && wave_lo <= hi && j0 <= wave_hi &&
                      (p.window <= 0 || j0 + TK - 1 > max(wave_lo, 0) - p.window || j0 < p.sinks);
     // the next tile's copies run between this one's products: one after the
     // other they would wait for the way into LDS
     const bool between = any && next.there == ~0ull && even;
     if (!between) fetch(next, stage_at(stage ^ 1));
     if (any) {
-      const char* kt = smem + 2 * stage * H::TILE;
+      const char* kt = ring + 2 * stage * H::TILE;
       const char* vt = kt + H::TILE;
       f32x16 s[2];
       bf16x8 a[NS][2];
@@ -961,23 +973,61 @@ __global__ __launch_bounds__(256, (D == 256 ? 1 : 2)) void prompt_kernel(AttnPar
 #pragma unroll
       for (int i = 0; i < NC; ++i) settle16(o[i]);
     }
-    now = then;
-    then = later;
-    later = after(later);
     here = next;
-    stage ^= 1;
   }
   attn_wait<0>();  // no copy may land after the workgroup's end
   l += __shfl_xor(l, 32);
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  if constexpr (GROUPS == 1) {
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    if (mine < t.n) {
+      bf16* out = (bf16*)((char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh) + 4 * half;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          store4<bf16>(out + 32 * i + 8 * j, o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
+                       o[i][4 * j + 3] * inv);
+    }
+    return;
+  } else {
+  // The join: each group ends up with one half of d.
+  lds_barrier();
+  f32x4* const box = (f32x4*)smem + wid * (H::box / 16);
+  float* const ml = (float*)(smem + 2 * H::NW * H::box) + wid * 128;
+#pragma unroll
+  for (int i = 0; i < NC / 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = group ? o[i][4 * j + e] : o[i + NC / 2][4 * j + e];
+      box[(4 * i + j) * 64 + lane] = v;
+    }
+  ml[lane] = m;
+  ml[64 + lane] = l;
+  lds_barrier();
+  const f32x4* const from_box = (const f32x4*)smem + (wid ^ 4) * (H::box / 16);
+  const float* const from_ml = (const float*)(smem + 2 * H::NW * H::box) + (wid ^ 4) * 128;
+  const float m2 = from_ml[lane], l2 = from_ml[64 + lane];
+  const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
+  float f1 = __builtin_amdgcn_exp2f(m - base), f2 = __builtin_amdgcn_exp2f(m2 - base);
+  const float all = l * f1 + l2 * f2, inv = all > 0.f || all != all ? 1.f / all : 0.f;
+  f1 *= inv;
+  f2 *= inv;
   if (mine < t.n) {
-    bf16* out = (bf16*)((char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh) + 4 * half;
+    bf16* out = (bf16*)((char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh) + group * (D / 2) + 4 * half;
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < NC / 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        store4<bf16>(out + 32 * i + 8 * j, o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
-                     o[i][4 * j + 3] * inv);
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 v = from_box[(4 * i + j) * 64 + lane];
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y[e] = (group ? o[i + NC / 2][4 * j + e] : o[i][4 * j + e]) * f1 + v[e] * f2;
+        store4<bf16>(out + 32 * i + 8 * j, y[0], y[1], y[2], y[3]);
+      }
+  }
   }
 }
 
@@ -985,15 +1035,22 @@ int64_t tiles_of(const AttnParams& p, int rows) {
   return p.cu ? (int64_t)p.t_total / rows + p.n_seq : (int64_t)p.n_seq * ((p.seq_len + rows - 1) / rows);
 }
 
+template <int D, int GROUPS>
+hipError_t launch_prompt(const AttnParams& p, int tiles, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)tiles * p.heads)), threads(256 * GROUPS);
+  if (p.table)
+    hipLaunchKernelGGL((prompt_kernel<D, true, GROUPS>), grid, threads, 0, s, p, tiles);
+  else
+    hipLaunchKernelGGL((prompt_kernel<D, false, GROUPS>), grid, threads, 0, s, p, tiles);
+  return hipGetLastError();
+}
+
 template <int D>
 hipError_t launch_prompt(const AttnParams& p, hipStream_t s) {
-  const int64_t tiles = tiles_of(p, PromptShape<D>::ROWS);
-  const dim3 grid((unsigned)(tiles * p.heads)), threads(256);
-  if (p.table)
-    hipLaunchKernelGGL((prompt_kernel<D, true>), grid, threads, 0, s, p, (int)tiles);
-  else
-    hipLaunchKernelGGL((prompt_kernel<D, false>), grid, threads, 0, s, p, (int)tiles);
-  return hipGetLastError();
+  const int tiles = (int)tiles_of(p, kPromptRows);
+  if constexpr (D <= 128)
+    if (getenv("GDN_SPLIT") ? atoi(getenv("GDN_SPLIT")) : (int64_t)tiles * p.heads <= 1024) return launch_prompt<D, 2>(p, tiles, s);
+  return launch_prompt<D, 1>(p, tiles, s);
 }
 
 template <typename TI, int D>
@@ -1008,7 +1065,7 @@ hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
 
 }  // namespace
 
-int attn_tile_rows(bool bf16_in, int) { return bf16_in ? 128 : 64; }
+int attn_tile_rows(bool bf16_in, int) { return bf16_in ? kPromptRows : 64; }
 hipError_t launch_attn_prefill(bool bf16_in, int d, const AttnParams& p, hipStream_t s) {
   if (d == 64) return bf16_in ? launch_prompt<64>(p, s) : launch_tiles<float, 64>(p, s);
   if (d == 128) return bf16_in ? launch_prompt<128>(p, s) : launch_tiles<float, 128>(p, s);
