@@ -599,6 +599,12 @@ __device__ __forceinline__ bool tile_rows(const AttnParams& p, int64_t i, int ro
   t.place = at;
   if (p.table) t.place += min(max(p.lens[t.seq], 0), p.max_len) - t.n;
   t.n = min(t.n - at, rows);
+  // (the same for all lanes, kept as scalars)
+  t.seq = __builtin_amdgcn_readfirstlane(t.seq);
+  t.start = __builtin_amdgcn_readfirstlane(t.start);
+  t.row = __builtin_amdgcn_readfirstlane(t.row);
+  t.n = __builtin_amdgcn_readfirstlane(t.n);
+  t.place = __builtin_amdgcn_readfirstlane(t.place);
   return true;
 }
 
