@@ -63,12 +63,28 @@ __device__ __forceinline__ void attn_copy4(uint32_t lds, const void* from) {
                : "memory", "m0");
 }
 
+// A value that is the same for all lanes, as a scalar.
+__device__ __forceinline__ uint64_t attn_scalar(uint64_t v) {
+  return ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+}
+
 // The same from a common address and a lane's offset to it.
 __device__ __forceinline__ void attn_copy16(uint32_t lds, const void* base, uint32_t offset) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"((uint64_t)(uintptr_t)base)
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(attn_scalar((uint64_t)(uintptr_t)base))
                : "memory", "m0");
+}
+
+// The same, or nothing.
+__device__ __forceinline__ void attn_copy16_if(bool go, uint32_t lds, const void* base, uint32_t offset) {
+  asm volatile("s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 .Lnot%=\n\ts_mov_b32 m0, %0\n\ts_nop 1\n\t"
+               "global_load_lds_dwordx4 %1, %2\n.Lnot%=:"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(attn_scalar((uint64_t)(uintptr_t)base)),
+                 "s"(__builtin_amdgcn_readfirstlane((int)go))
+               : "memory", "m0", "scc");
 }
 
 __device__ __forceinline__ uint32_t attn_lds(const void* p) {
@@ -753,11 +769,15 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
   const int mine = wave * 32 + col, place = lo + mine;
   const int wave_lo = lo + wave * 32, wave_hi = min(wave_lo + 31, hi);
 
+  // (the largest score is the largest product: a scale's sign goes to q)
+  const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+  const float scale = fabsf(p.scale);
   bf16x8 q[NS];
 #pragma unroll
   for (int u = 0; u < NS; ++u) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (mine < t.n) v = ld16((const char*)p.q + (int64_t)(t.row + mine) * p.q_st + h * p.q_sh + (2 * u + half) * 16);
+    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
     q[u] = __builtin_bit_cast(bf16x8, v);
   }
   f32x16 o[NC];
@@ -796,10 +816,12 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
   // lanes' offsets that stay; others row by row.
   constexpr int PR = 64 / GR;
   const bool even = !PAGED || p.page.d % PR == 0;
-  uint32_t k_off[P], v_off[P];
+  constexpr int STEP = H::NW * PR;          // rows to the wave's next piece
+  constexpr int KINDS = STEP % 16 ? 2 : 1;  // of swizzles among its pieces
+  uint32_t k_off[KINDS], v_off[KINDS];
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int r = (i * H::NW + wave) * PR + lane / GR, row = PAGED ? lane / GR : r;
+  for (int i = 0; i < KINDS; ++i) {
+    const int r = i * STEP + wave * PR + lane / GR, row = PAGED ? lane / GR : wave * PR + lane / GR;
     const uint32_t g = ((lane % GR) ^ attn_swz<GR>(r)) * 16;
     k_off[i] = (uint32_t)row * (uint32_t)p.k_st + g;
     v_off[i] = (uint32_t)row * (uint32_t)p.v_st + g;
@@ -824,27 +846,35 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
     w.there = __ballot(is);
     return w;
   };
-  // Piece i of a tile that is there as a whole: keys, then values.
-  const auto copy = [&](const Where& w, uint32_t to, int i) {
-    int64_t ko, vo;
+  // Piece i of a tile that is there as a whole, keys first (`go` false:
+  // nothing); all pieces of any tile.  Without pages a tile's pieces follow
+  // each other by a stride.
+  const int64_t k_step = STEP * p.k_st, v_step = STEP * p.v_st;
+  const char *k_now = nullptr, *v_now = nullptr;
+  const auto start = [&](const Where& w) __attribute__((always_inline)) {
+    if (PAGED) return;
+    k_now = k_base + (int64_t)(t.start + w.tile * TK) * p.k_st;
+    v_now = v_base + (int64_t)(t.start + w.tile * TK) * p.v_st;
+  };
+  const auto copy = [&](const Where& w, uint32_t to, int i, bool go) __attribute__((always_inline)) {
+    const bool values = i >= P;
+    if (values) i -= P;
+    const char* from;
     if (PAGED) {
-      const int r = (i * H::NW + wave) * PR, at = w.tile * TK + r;
+      const int r = i * STEP + wave * PR, at = w.tile * TK + r;
       const int pg = __builtin_amdgcn_readlane(w.page, r), in = at - attn_quotient(p.page, at) * (int)p.page.d;
-      ko = pg * p.k_sp + in * p.k_st;
-      vo = pg * p.v_sp + in * p.v_st;
+      from = values ? v_base + (pg * p.v_sp + in * p.v_st) : k_base + (pg * p.k_sp + in * p.k_st);
+    } else if (values) {
+      from = v_now;
+      v_now += v_step;
     } else {
-      ko = (int64_t)(t.start + w.tile * TK) * p.k_st;
-      vo = (int64_t)(t.start + w.tile * TK) * p.v_st;
+      from = k_now;
+      k_now += k_step;
     }
-    attn_copy16(to + i * H::NW * 1024, k_base + ko, k_off[i]);
-    attn_copy16(to + i * H::NW * 1024 + H::TILE, v_base + vo, v_off[i]);
+    attn_copy16_if(go, to + i * H::NW * 1024 + (values ? H::TILE : 0), from,
+                   values ? v_off[i % KINDS] : k_off[i % KINDS]);
   };
   const auto fetch = [&](const Where& w, uint32_t to) {
-    if (w.there == ~0ull && even) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) copy(w, to, i);
-      return;
-    }
     const int j = w.tile * TK + lane;
     int64_t ko, vo;
     if (PAGED) {
@@ -857,7 +887,7 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int r = (i * H::NW + wave) * PR + lane / GR;
+      const int r = i * STEP + wave * PR + lane / GR;
       const int64_t kr = __shfl(ko, r), vr = __shfl(vo, r);
       const int g = ((lane % GR) ^ attn_swz<GR>(r)) * 16;
       const bool is = (w.there >> r) & 1u;
@@ -880,56 +910,43 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
   Where here = look(tile_at(0), 0);
   fetch(here, stage_at(0));
   ask(tile_at(1), 1);
-  f32x16 none;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) none[e] = 0.f;
-  settle16(none);
+  // Tiles that every query of the workgroup sees as a whole, the group's next
+  // one there as a whole too: nothing is looked up for them.
+  const int plain_from = p.window > 0 ? max(from, (hi - p.window >= 0 ? (hi - p.window) / TK + 1 : 0)) : 0;
+  const int plain_to = min((max(lo, -1) + 1) / TK, (max(hi, -1) + 1) / TK - GROUPS);
   for (int j = 0; j < turns; ++j) {
     const int stage = j & 1;
     attn_wait_lds();
     ask(tile_at(j + 2), stage);
     attn_wait<PAGED ? 1 : 0>();
     lds_barrier();
-    const Where next = look(tile_at(j + 1), stage ^ 1);
     const int j0 = here.tile * TK;
-    const bool any = here.tile < end && wave_lo <= hi && j0 <= wave_hi &&
-                     (p.window <= 0 || j0 + TK - 1 > max(wave_lo, 0) - p.window || j0 < p.sinks);
-    // the next tile's copies run between this one's products: one after the
-    // other they would wait for the way into LDS
-    const bool between = any && next.there == ~0ull && even;
-    if (!between) fetch(next, stage_at(stage ^ 1));
+    const bool plain = !PAGED && here.tile >= plain_from && here.tile < plain_to;
+    Where next{here.tile + GROUPS, 0, ~0ull};
+    if (!plain) next = look(tile_at(j + 1), stage ^ 1);
+    const bool whole = plain || (j0 + TK - 1 <= wave_lo && here.there == ~0ull &&
+                                 (p.window <= 0 || j0 > wave_hi - p.window || j0 + TK <= p.sinks));
+    const bool any = whole || (here.tile < end && wave_lo <= hi && j0 <= wave_hi &&
+                               (p.window <= 0 || j0 + TK - 1 > max(wave_lo, 0) - p.window || j0 < p.sinks));
+    const uint32_t to = stage_at(stage ^ 1);
+    const bool go = any && next.there == ~0ull && even;
+    start(next);
+    if (!go) {
+      if (next.there == ~0ull && even) {
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i) copy(next, to, i, true);
+      } else {
+        fetch(next, to);
+      }
+    }
     if (any) {
       const char* kt = ring + 2 * stage * H::TILE;
       const char* vt = kt + H::TILE;
-      f32x16 s[2];
-      bf16x8 a[NS][2];
       const auto key = [&](int u, int b) { return *(const bf16x8*)(kt + (k_at ^ (u * 32)) + b * 32 * RB); };
-      constexpr int AHEAD = 4, EVERY = NS / P;  // operands on their way; products to a copy
-#pragma unroll
-      for (int u = 0; u < AHEAD; ++u)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) a[u][b] = key(u, b);
-#pragma unroll
-      for (int u = 0; u < NS; ++u) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[u][b], q[u], u == 0 ? none : s[b], 0, 0, 0);
-          if (u + AHEAD < NS) a[u + AHEAD][b] = key(u + AHEAD, b);
-        }
-        if (u % EVERY == 0 && between) copy(next, stage_at(stage ^ 1), u / EVERY);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      settle16(s[0]);
-      settle16(s[1]);
       const auto value = [&](int u, int i) {
         return ssm_tr(vt + (v_at0 ^ (i * 64)) + u * 16 * RB, vt + (v_at1 ^ (i * 64)) + u * 16 * RB);
       };
-      bf16x8 first[NC];  // the first of V's operands, asked for early
-#pragma unroll
-      for (int i = 0; i < NC; ++i) first[i] = value(0, i);
-      const bool whole = j0 + TK - 1 <= wave_lo && here.there == ~0ull &&
-                         (p.window <= 0 || j0 > wave_hi - p.window || j0 + TK <= p.sinks);
-      if (!whole) {
+      const auto hide = [&](f32x16 (&s)[2]) __attribute__((always_inline)) {
         // the keys that the lane's query sees, a bit each
         uint64_t see = here.there & low_bits(place - j0 + 1);
         if (p.window > 0) see &= ~low_bits(place - j0 - p.window + 1) | low_bits(p.sinks - j0);
@@ -939,45 +956,169 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             s[b][e] = ((uint32_t)(see >> (32 * b)) >> (8 * (e >> 2) + (e & 3))) & 1u ? s[b][e] : -INFINITY;
-      }
-      float top = s[0][0];
+      };
+      if constexpr (D < 256) {
+        constexpr int AHEAD = NS < 6 ? NS : 6;  // pairs of operands on their way
+        f32x16 s[2];
+        bf16x8 a[NS][2], first[NC], w[4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int e = 0; e < 32; ++e) s[e >> 4][e & 15] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
-      top = max_halves(top) * p.scale;
-      // O and l are rescaled only where the maximum has grown by more than
-      // 2^8: weights of up to 2^8 lose nothing in fp32 or bf16
-      if (__any(top > m + 8.f)) {
-        const float next = fmaxf(m, top);
-        const float keep = __builtin_amdgcn_exp2f(m - (next == -INFINITY ? 0.f : next));
-        m = next;
-        l *= keep;
+        for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
+          for (int b = 0; b < 2; ++b) a[u][b] = key(u, b);
+        // the next tile's copies run between this one's products: one after the
+        // other they would wait for the way into LDS
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[i][e] *= keep;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      float sum = 0.f;
-      bf16x8 w[4];
+        for (int u = 0; u < NS; ++u) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float x = __builtin_amdgcn_exp2f(s[b][e] * p.scale - base);
-          sum += x;
-          w[2 * b + (e >> 3)][e & 7] = (bf16)x;
+          for (int b = 0; b < 2; ++b) {
+            s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[u][b], q[u], s[b], 0, 0, 0);
+            if (u + AHEAD < NS) a[u + AHEAD][b] = key(u + AHEAD, b);
+          }
+          if (u < 2 * P) copy(next, to, u, go);
+          __builtin_amdgcn_sched_barrier(0);
         }
-      l += sum;
+        // (the first of V's operands, asked for early)
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+        for (int i = 0; i < NC; ++i) first[i] = value(0, i);
+        settle16(s[0]);
+        settle16(s[1]);
+        if (!whole) hide(s);
+        float top = s[0][0];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u == 0 ? first[i] : value(u, i), w[u], o[i], 0, 0, 0);
+        for (int n = 1; n < 32; ++n) top = fmaxf(top, s[n >> 4][n & 15]);
+        // O and l are rescaled only where the maximum has grown by more than 2^8:
+        // weights of up to 2^8 lose nothing in fp32 or bf16
+        if (__any(top * scale > m + 8.f)) {
+          const float up = fmaxf(m, max_halves(top) * scale);
+          const float keep = __builtin_amdgcn_exp2f(m - (up == -INFINITY ? 0.f : up));
+          m = up;
+          l *= keep;
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[i][e] *= keep;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < 32; ++n) {
+          const float x = __builtin_amdgcn_exp2f(s[n >> 4][n & 15] * scale - base);
+          sum[n & 1] += x;
+          w[n >> 3][n & 7] = (bf16)x;
+        }
+        l += sum[0] + sum[1];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u == 0 ? first[i] : value(u, i), w[u], o[i], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) settle16(o[i]);
+      } else {
+        // A wave alone on its SIMD: half a tile's softmax beside the products of the
+        // other half's scores, the other half's beside those of the first one's
+        // values (4096 tokens x 16 heads 186 us, one after the other 203; with two
+        // waves a SIMD, d = 128, 100.3 and 98.1).  The products' operands are read
+        // in their order, AHEAD of them on their way.
+        constexpr int NK = 2 * NS, NV = 4 * NC, AHEAD = 8;
+        f32x16 s[2];
+        bf16x8 a[NK + NV], w[4];
+        const auto read = [&](int n) __attribute__((always_inline)) {
+          if (n < NK) a[n] = key(n % NS, n / NS);
+          else if (n < NK + NV) a[n] = value((n - NK) / NC, (n - NK) % NC);
+        };
+        float top[2], sum[2];
+        const float before = m == -INFINITY ? 0.f : m;
+        // The weights of the 16 scores of half b against a maximum, in steps of
+        // `part`: a step forms exponents, the next one their powers, the one
+        // after sums and rounds them, so that none waits for the one before.
+        float y[16];
+        const auto weigh = [&](int b, int step, int part, float base) __attribute__((always_inline)) {
+#pragma unroll
+          for (int e = step * part; e < min(16, (step + 1) * part); ++e) {
+            y[e] = s[b][e] * scale - base;
+            if (b == 0) top[0] = e == 0 ? s[0][0] : fmaxf(top[0], s[0][e]);
+          }
+          if (step > 0) {
+#pragma unroll
+            for (int e = (step - 1) * part; e < min(16, step * part); ++e) y[e] = __builtin_amdgcn_exp2f(y[e]);
+          }
+          if (step > 1) {
+#pragma unroll
+            for (int e = (step - 2) * part; e < min(16, (step - 1) * part); ++e) {
+              sum[b] = e == 0 ? y[0] : sum[b] + y[e];
+              w[2 * b + (e >> 3)][e & 7] = (bf16)y[e];
+            }
+          }
+        };
+#pragma unroll
+        for (int n = 0; n < 32; ++n) s[n >> 4][n & 15] = 0.f;
+#pragma unroll
+        for (int f = 0; f < AHEAD; ++f) read(f);
+        // the scores of 32 keys, then of the other 32 beside the first ones'
+        // weights; the next tile's copies between them
+        constexpr int STEPS = NS - 3, PART = (16 + STEPS - 1) / STEPS;
+#pragma unroll
+        for (int f = 0; f < 2 * NS; ++f) {
+          s[f / NS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[f], q[f % NS], s[f / NS], 0, 0, 0);
+          read(f + AHEAD);
+          if (f < 2 * P) copy(next, to, f, go);
+          if (f > NS) weigh(0, f - NS - 1, PART, before);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(sum[0]), "+v"(top[0]));  // (weighed here, not behind the branch)
+        settle16(s[0]);
+        settle16(s[1]);
+        if (!whole) hide(s);
+        top[1] = s[1][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top[1] = fmaxf(top[1], s[1][e]);
+        // O and l are rescaled only where the maximum has grown by more than 2^8:
+        // weights of up to 2^8 lose nothing in fp32 or bf16
+        bool redo = false;  // (a flag: a branch over both would have O copied)
+        if (!whole || __any(fmaxf(top[0], top[1]) * scale > m + 8.f)) {
+          top[0] = s[0][0];
+#pragma unroll
+          for (int e = 1; e < 16; ++e) top[0] = fmaxf(top[0], s[0][e]);
+          const float up = fmaxf(m, max_halves(fmaxf(top[0], top[1])) * scale);
+          const float keep = __builtin_amdgcn_exp2f(m - (up == -INFINITY ? 0.f : up));
+          m = up;
+          l *= keep;
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[i][e] *= keep;
+          redo = true;
+        }
+        if (redo) {
+#pragma unroll
+          for (int i = 0; i < 3; ++i) weigh(0, i, 16, m == -INFINITY ? 0.f : m);
+        }
+        l += sum[0];
+        // the first 32 keys' values beside the other ones' weights
+        const float base = m == -INFINITY ? 0.f : m;
+        constexpr int STEPS1 = 2 * NC - 3, PART1 = (16 + STEPS1 - 1) / STEPS1;
+#pragma unroll
+        for (int f = 0; f < 2 * NC; ++f) {
+          const int u = f / NC, i = f % NC;
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[NK + f], w[u], o[i], 0, 0, 0);
+          read(NK + f + AHEAD);
+          if (f > 0) weigh(1, f - 1, PART1, base);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        l += sum[1];
+#pragma unroll
+        for (int f = 0; f < 2 * NC; ++f) {
+          const int u = 2 + f / NC, i = f % NC;
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[NK + 2 * NC + f], w[u], o[i], 0, 0, 0);
+          read(NK + 2 * NC + f + AHEAD);
+          __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-      for (int i = 0; i < NC; ++i) settle16(o[i]);
+        for (int i = 0; i < NC; ++i) settle16(o[i]);
+      }
     }
     here = next;
   }
@@ -996,44 +1137,44 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
     }
     return;
   } else {
-  // The join: each group ends up with one half of d.
-  lds_barrier();
-  f32x4* const box = (f32x4*)smem + wid * (H::box / 16);
-  float* const ml = (float*)(smem + 2 * H::NW * H::box) + wid * 128;
-#pragma unroll
-  for (int i = 0; i < NC / 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f32x4 v;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = group ? o[i][4 * j + e] : o[i + NC / 2][4 * j + e];
-      box[(4 * i + j) * 64 + lane] = v;
-    }
-  ml[lane] = m;
-  ml[64 + lane] = l;
-  lds_barrier();
-  const f32x4* const from_box = (const f32x4*)smem + (wid ^ 4) * (H::box / 16);
-  const float* const from_ml = (const float*)(smem + 2 * H::NW * H::box) + (wid ^ 4) * 128;
-  const float m2 = from_ml[lane], l2 = from_ml[64 + lane];
-  const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
-  float f1 = __builtin_amdgcn_exp2f(m - base), f2 = __builtin_amdgcn_exp2f(m2 - base);
-  const float all = l * f1 + l2 * f2, inv = all > 0.f || all != all ? 1.f / all : 0.f;
-  f1 *= inv;
-  f2 *= inv;
-  if (mine < t.n) {
-    bf16* out = (bf16*)((char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh) + group * (D / 2) + 4 * half;
+    // The join: each group ends up with one half of d.
+    lds_barrier();
+    f32x4* const box = (f32x4*)smem + wid * (H::box / 16);
+    float* const ml = (float*)(smem + 2 * H::NW * H::box) + wid * 128;
 #pragma unroll
     for (int i = 0; i < NC / 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x4 v = from_box[(4 * i + j) * 64 + lane];
-        float y[4];
+        f32x4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y[e] = (group ? o[i + NC / 2][4 * j + e] : o[i][4 * j + e]) * f1 + v[e] * f2;
-        store4<bf16>(out + 32 * i + 8 * j, y[0], y[1], y[2], y[3]);
+        for (int e = 0; e < 4; ++e) v[e] = group ? o[i][4 * j + e] : o[i + NC / 2][4 * j + e];
+        box[(4 * i + j) * 64 + lane] = v;
       }
-  }
+    ml[lane] = m;
+    ml[64 + lane] = l;
+    lds_barrier();
+    const f32x4* const from_box = (const f32x4*)smem + (wid ^ 4) * (H::box / 16);
+    const float* const from_ml = (const float*)(smem + 2 * H::NW * H::box) + (wid ^ 4) * 128;
+    const float m2 = from_ml[lane], l2 = from_ml[64 + lane];
+    const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.f : top;
+    float f1 = __builtin_amdgcn_exp2f(m - base), f2 = __builtin_amdgcn_exp2f(m2 - base);
+    const float all = l * f1 + l2 * f2, inv = all > 0.f || all != all ? 1.f / all : 0.f;
+    f1 *= inv;
+    f2 *= inv;
+    if (mine < t.n) {
+      bf16* out = (bf16*)((char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh) + group * (D / 2) + 4 * half;
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 v = from_box[(4 * i + j) * 64 + lane];
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = (group ? o[i + NC / 2][4 * j + e] : o[i][4 * j + e]) * f1 + v[e] * f2;
+          store4<bf16>(out + 32 * i + 8 * j, y[0], y[1], y[2], y[3]);
+        }
+    }
   }
 }
 
@@ -1054,8 +1195,14 @@ hipError_t launch_prompt(const AttnParams& p, int tiles, hipStream_t s) {
 template <int D>
 hipError_t launch_prompt(const AttnParams& p, hipStream_t s) {
   const int tiles = (int)tiles_of(p, kPromptRows);
+  // Few workgroups: the last one's time is the whole call's, and one that is
+  // alone on its compute unit leaves half of it idle.  Measured, two groups and
+  // one, d = 128: one prompt of 4096 tokens x 16 heads (512 workgroups) 90 and 98
+  // us, 2048 x 16 35 and 43, 8192 x 8 143 and 170; of 4096 x 32 (1024) 157 and
+  // 152; with a window, whose tiles are alike, 2048 x 16 (256) 20.4 and 20.5,
+  // 8192 x 16 (1024) 76 and 58.
   if constexpr (D <= 128)
-    if (getenv("GDN_SPLIT") ? atoi(getenv("GDN_SPLIT")) : (int64_t)tiles * p.heads <= 1024) return launch_prompt<D, 2>(p, tiles, s);
+    if ((int64_t)tiles * p.heads <= (p.window > 0 ? 256 : 512)) return launch_prompt<D, 2>(p, tiles, s);
   return launch_prompt<D, 1>(p, tiles, s);
 }
 

@@ -21,6 +21,7 @@ namespace {
 constexpr int64_t kMaxThreads = (int64_t)1 << 32;  // of one launch
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxRequests = (int64_t)1 << 20;
+constexpr int64_t kMaxRowStride = (int64_t)1 << 24;  // keys' and values': 32-bit offsets inside a tile
 
 bool attn_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
@@ -90,7 +91,7 @@ bool interleaved(const gdn_tensor* a, const gdn_tensor* b) {
 int attn_options(const gdn_attn_options* opts, gdn_attn_options* o) {
   gdn_attn_default_options(o);
   if (opts) *o = *opts;
-  if (!std::isfinite(o->scale)) return api_fail(GDN_ERR_SHAPE, "scale must be finite");
+  if (!(std::fabs(o->scale) <= 0x1p64f)) return api_fail(GDN_ERR_SHAPE, "scale must be within +-2^64");
   if (o->window < 0) return api_fail(GDN_ERR_SHAPE, "window must be >= 0 (got %d)", o->window);
   if (o->sinks < 0) return api_fail(GDN_ERR_SHAPE, "sinks must be >= 0 (got %d)", o->sinks);
   return GDN_OK;
@@ -125,6 +126,9 @@ int check_heads(const Attn& A, const gdn_tensor* q, const gdn_tensor* k, const g
     return api_fail(GDN_ERR_SHAPE, "query heads (%lld) must be a positive multiple of key heads (%lld)", (long long)A.H,
                     (long long)A.K);
   if (A.H > 65535) return api_fail(GDN_ERR_UNSUPPORTED, "at most 65535 heads");
+  const int row = k->ndim - 3;
+  if (!is_empty(k) && k->shape[row] > 1 && std::max(k->stride[row], v->stride[row]) > kMaxRowStride)
+    return api_fail(GDN_ERR_LAYOUT, "tokens of k and v lie at most 2^24 elements apart");
   int rc;
   if ((rc = check_granules(q, "q")) || (rc = check_granules(k, "k")) || (rc = check_granules(v, "v")) ||
       (rc = check_granules(out, "out")))

@@ -692,11 +692,12 @@ int gdn_cache_store(const gdn_tensor* k, const gdn_tensor* v, const gdn_tensor* 
  * enter the product with v in bf16 (prompts: one term; single tokens: two).
  * Inputs of what is seen are expected to be finite: a NaN or infinity in a
  * key or value reaches the rows that see it and may reach earlier rows of its
- * own sequence in the same tile of 256; none reaches another sequence, and
- * what lies in the cache behind a sequence's length is never read.
+ * own sequence in the same tile of 128 queries; none reaches another sequence,
+ * and what lies in the cache behind a sequence's length is never read.
  */
 typedef struct gdn_attn_options {
-  float scale;     /* multiplies the scores; 0 (default): 1 / sqrt(d)         */
+  float scale;     /* multiplies the scores, within +-2^64; 0 (default):
+                      1 / sqrt(d)                                             */
   int32_t window;  /* keys that a query sees, its own among them; 0: all      */
   int32_t sinks;   /* first tokens that every query sees beside its window    */
 } gdn_attn_options;
@@ -716,7 +717,8 @@ void gdn_attn_default_options(gdn_attn_options* opts);
  *               query before a sequence's first token sees none
  *   block_table, seq_lens  [N, M], [N] int32, or both NULL
  *   opts        NULL for the defaults
- * d in {64, 128, 256}; unit stride in d, other strides multiples of 16 bytes.
+ * d in {64, 128, 256}; unit stride in d, other strides multiples of 16 bytes;
+ * tokens of k and v at most 2^24 elements apart.
  */
 int gdn_attn_prefill(const gdn_tensor* q, const gdn_tensor* k, const gdn_tensor* v,
                      const gdn_tensor* cu_seqlens, const gdn_tensor* block_table,

@@ -284,3 +284,21 @@ def test_prefill_a_step_at_a_time_is_decode():
         out = G.gdn_attn_decode(q[t:t + 1].cuda(), kc, vc, table, i32([t + 1]).cuda())
         check(out, ref[0][t:t + 1], bound(torch.float32, *(x[t:t + 1] for x in ref), True), f"token {t}")
     check_out(whole, ref, torch.float32, "whole")
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 64), (torch.bfloat16, 128), (torch.bfloat16, 256), (torch.float32, 128)])
+@pytest.mark.parametrize("scale", [0.02, -0.2])
+def test_prefill_scale(dtype, d, scale):
+    prefill(70, [300, 1, 77], 4, 2, d, dtype, scale=scale)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lengths,H", [([300], 128), ([4000], 16), ([4225], 16), ([200, 0, 3300, 9], 20)])
+def test_prefill_around_the_split(d, lengths, H):
+    """Few and many (tile, head) pairs: keys shared by two groups of waves, or not."""
+    prefill(71, lengths, H, 2, d, torch.bfloat16)
+
+
+@pytest.mark.parametrize("lengths", [[8193], [2048, 17, 900]])
+def test_prefill_window_around_the_split(lengths):
+    prefill(72, lengths, 4, 2, 128, torch.bfloat16, window=130, sinks=70)
