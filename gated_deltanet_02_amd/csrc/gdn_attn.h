@@ -83,7 +83,8 @@ struct AttnParams {
   // gdn_attn_decode: what its parts leave for the join
   float* parts;
   int32_t* chains;
-  int32_t waves;  // that share the work
+  int32_t waves, waves_log2;  // that share the work, a power of two
+  int32_t by_pair;            // chains lie by their pair, else by their first wave
 };
 
 hipError_t launch_cache_plan(const PlanParams& p, hipStream_t s);

@@ -167,7 +167,7 @@ struct AttnCore {
     for (int i = 0; i < NC; ++i) o[i] = zero4();
   }
   // the queries' rows, or zeros
-  __device__ __forceinline__ void load(const char* row, bool live, int lane) {
+  static __device__ __forceinline__ void load(U (&q)[NU], const char* row, bool live, int lane) {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -282,36 +282,49 @@ struct StepShape {
   static_assert(total <= 163840 && NW >= 1 && NW <= 16, "LDS");
 };
 
-// A tile of the list: its pair, the first of its keys among those that the
-// sequence's query sees, and how many those are.
+// A tile of the list: its pair, its number among the pair's, and what that
+// pair's query sees: the tiles of the sinks, then those from `from` on.
 struct StepTile {
-  int seq, unit, tile, tiles;
-  int seen, gap;  // keys from `sinks` on lie `gap` further behind
+  int seq, unit, kh, tile, tiles;
+  int len, low, from, sink_tiles;  // low: the last key before the window
+  __device__ __forceinline__ int first() const { return tile < sink_tiles ? tile : from + tile - sink_tiles; }
 };
 
 struct StepWork {
   const AttnParams& p;
   int units, blocks, keys;
-  __device__ __forceinline__ int seen(int len) const {
-    return p.window > 0 ? (int)min((int64_t)len, (int64_t)p.window + p.sinks) : len;
+  __device__ __forceinline__ int from(int len) const { return p.window > 0 ? max(0, len - p.window) / keys : 0; }
+  __device__ __forceinline__ int sinks(int len) const {
+    return p.window > 0 ? min((min(p.sinks, len) + keys - 1) / keys, from(len)) : 0;
   }
-  __device__ __forceinline__ int tiles(int len) const { return (seen(len) + keys - 1) / keys; }
+  __device__ __forceinline__ int tiles(int len) const {
+    return sinks(len) + len / keys + (len % keys ? 1 : 0) - from(len);
+  }
   __device__ __forceinline__ int lane_len(int64_t i) const {
-    return i < p.n_seq ? min(max(p.lens[i], 0), p.max_len) : 0;
+    return min(max(p.lens[min(i, (int64_t)p.n_seq - 1)], 0), i < p.n_seq ? p.max_len : 0);
+  }
+  __device__ __forceinline__ void turn(StepTile& x, int unit) const {
+    x.unit = unit;
+    x.kh = blocks == 1 ? unit : unit / blocks;
   }
   __device__ __forceinline__ void enter(StepTile& x, int seq) const {
     const int len = attn_len(p, seq);
     x.seq = seq;
-    x.seen = seen(len);
-    x.gap = len - x.seen;
-    x.tiles = (x.seen + keys - 1) / keys;
+    x.len = len;
+    x.low = p.window > 0 ? len - 1 - p.window : -1;
+    x.from = from(len);
+    x.sink_tiles = sinks(len);
+    x.tiles = tiles(len);
   }
   // The next tile of the list (there is one).
   __device__ __forceinline__ void next(StepTile& x, int lane) const {
     if (++x.tile < x.tiles) return;
     x.tile = 0;
-    if (++x.unit < units) return;
-    x.unit = 0;
+    if (x.unit + 1 < units) {
+      turn(x, x.unit + 1);
+      return;
+    }
+    turn(x, 0);
     int seq = x.seq + 1;
     if (attn_len(p, seq) == 0) {  // empty ones, 64 at a time
       uint64_t some;
@@ -339,7 +352,8 @@ __device__ __forceinline__ int64_t wave_pick(int64_t v, int lane) {
 template <typename TI, int D>
 __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnParams p) {
   using H = StepShape<TI, D>;
-  constexpr int TT = H::TT, TW = H::TW, RB = H::RB, GR = H::GR, P = H::PIECES;
+  using Core = AttnCore<TI, D, H::TT>;
+  constexpr int TT = H::TT, TW = H::TW, GR = H::GR, P = H::PIECES, PR = 64 / GR;
   __shared__ __attribute__((aligned(1024))) char smem[H::total];
   const int lane = threadIdx.x & 63;
   const int in_group = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -355,10 +369,16 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
   // [l c, (l + 1) c), c a 64th of all
   const int64_t c = ((int64_t)p.n_seq + 63) / 64;
   int64_t sum = 0;
-  for (int64_t i = lane * c; i < (lane + 1) * c; ++i) sum += w.tiles(w.lane_len(i));
+  for (int64_t i = lane * c; i < (lane + 1) * c; i += 8) {
+    int len[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) len[k] = w.lane_len(i + k);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += i + k < (lane + 1) * c ? w.tiles(len[k]) : 0;
+  }
   const int64_t upto = wave_upto(sum, lane);
   const int64_t all = wave_pick(upto, 63) * w.units;
-  const int64_t each = all / p.waves, more = all - each * p.waves;
+  const int64_t each = all >> p.waves_log2, more = all - (each << p.waves_log2);
   const int64_t a = wave * each + min((int64_t)wave, more), b = a + each + (wave < more ? 1 : 0);
   int chain = 0, chain_seq = 0, chain_unit = 0;
 
@@ -370,88 +390,106 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
       const int at = __ffsll((unsigned long long)past) - 1;
       int64_t before = wave_pick(upto - sum, at);
       int64_t i0 = at * c;
-      int64_t mine, inner;
-      uint64_t hit;
-      for (;;) {  // the sequence among the lane's, 64 at a time
-        mine = i0 + lane < (at + 1) * c ? w.tiles(w.lane_len(i0 + lane)) : 0;
-        inner = wave_upto(mine, lane);
-        hit = __ballot((before + inner) * w.units > a);
-        if (hit) break;
-        before += wave_pick(inner, 63);
-        i0 += 64;
+      if (c > 1) {  // the sequence among the lane's, 64 at a time
+        int64_t mine, inner;
+        uint64_t hit;
+        for (;;) {
+          mine = i0 + lane < (at + 1) * c ? w.tiles(w.lane_len(i0 + lane)) : 0;
+          inner = wave_upto(mine, lane);
+          hit = __ballot((before + inner) * w.units > a);
+          if (hit) break;
+          before += wave_pick(inner, 63);
+          i0 += 64;
+        }
+        const int k = __ffsll((unsigned long long)hit) - 1;
+        before += wave_pick(inner - mine, k);
+        i0 += k;
       }
-      const int k = __ffsll((unsigned long long)hit) - 1;
-      before += wave_pick(inner - mine, k);
-      w.enter(x, __builtin_amdgcn_readfirstlane((int)(i0 + k)));
+      w.enter(x, __builtin_amdgcn_readfirstlane((int)i0));
       const int64_t rest = a - before * w.units;
-      x.unit = __builtin_amdgcn_readfirstlane((int)(rest / x.tiles));
-      x.tile = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)x.unit * x.tiles));
+      const int unit = rest >> 31 ? (int)(rest / x.tiles) : (int)((uint32_t)rest / (uint32_t)x.tiles);
+      w.turn(x, __builtin_amdgcn_readfirstlane(unit));
+      x.tile = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)unit * x.tiles));
       first = a - x.tile;
     }
 
+    const auto live = [&](const StepTile& t, int j) { return j < t.len && (j > t.low || j < p.sinks); };
     // The table's entries of a tile, one a lane, into one of two rows.
-    const auto place = [&](const StepTile& t, int i) { return i < p.sinks || t.gap == 0 ? i : i + t.gap; };
-    const auto ask = [&](const StepTile& t, bool live, int row) {
-      const int i = t.tile * TW + lane;
+    const auto ask = [&](const StepTile& t, bool go, int row) {
+      const int j = t.first() * TW + lane;
       const void* from = p.lens;
-      if (live && lane < TW && i < t.seen)
-        from = p.table + t.seq * p.table_st + attn_quotient(p.page, place(t, i));
+      if (go && lane < TW && live(t, j)) from = p.table + t.seq * p.table_st + attn_quotient(p.page, j);
       attn_copy4(entries_at + row * 256, from);
     };
     // The keys, then the values of a tile whose entries have come; which of
-    // its keys there are.
-    const auto fetch = [&](const StepTile& t, bool live, int row, int stage) -> uint32_t {
-      const int i = t.tile * TW + lane;
-      int page = -1, in = 0;
-      if (live && lane < TW && i < t.seen) {
-        const int at = place(t, i);
-        page = entries[row * 64 + lane];
-        if ((uint32_t)page >= (uint32_t)p.pages) page = -1;
-        in = at - attn_quotient(p.page, at) * (int)p.page.d;
-      }
-      const uint32_t there = (uint32_t)__ballot(page >= 0);
-      const int kh = t.unit / w.blocks;
+    // its keys there are.  Where all are and pages keep a piece's PR rows
+    // together, a piece's address is its first row's and lanes' offsets to
+    // it; else each lane has an address of its own.
+    const bool even = p.page.d % PR == 0;
+    const uint32_t g0 = ((lane % GR) ^ attn_swz<GR>(lane / GR)) * 16;
+    const uint32_t k_row = lane / GR * (uint32_t)p.k_st, v_row = lane / GR * (uint32_t)p.v_st;
+    const auto fetch = [&](const StepTile& t, bool go, int row, int stage) -> uint32_t {
+      const int j = t.first() * TW + lane;
+      const int in = j - attn_quotient(p.page, j) * (int)p.page.d;
+      const int page = entries[row * 64 + (lane & (TW - 1))];
+      const uint32_t there =
+          (uint32_t)__ballot(go && lane < TW && live(t, j) && (uint32_t)page < (uint32_t)p.pages);
+      const uint64_t ka = (uint64_t)(uintptr_t)p.k + t.kh * p.k_sh + page * p.k_sp + in * p.k_st;
+      const uint64_t va = (uint64_t)(uintptr_t)p.v + t.kh * p.v_sh + page * p.v_sp + in * p.v_st;
+      const uint32_t to = ring_at + 2 * stage * H::TILE;
+      if (even && there == (TW == 32 ? 0xffffffffu : 0xffffu)) {
 #pragma unroll
-      for (int kind = 0; kind < 2; ++kind) {
-        const char* base = kind ? (const char*)p.v + kh * p.v_sh : (const char*)p.k + kh * p.k_sh;
-        const int64_t sp = kind ? p.v_sp : p.k_sp, st = kind ? p.v_st : p.k_st;
+        for (int kind = 0; kind < 2; ++kind)
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const int r = j * (64 / GR) + lane / GR;
-          const int pg = __shfl(page, r), pl = __shfl(in, r);
-          const char* from = base + pg * sp + pl * st + (((lane % GR) ^ attn_swz<GR>(r)) * 16);
-          attn_copy16(ring_at + (2 * stage + kind) * H::TILE + j * 1024, pg >= 0 ? from : (const char*)attn_zeros);
-        }
+          for (int i = 0; i < P; ++i)
+            attn_copy16(to + kind * H::TILE + i * 1024, (const void*)(uintptr_t)wave_pick(kind ? va : ka, i * PR),
+                        (g0 ^ (attn_swz<GR>(i * PR) * 16)) + (kind ? v_row : k_row));
+      } else {
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int r = i * PR + lane / GR;
+            const uint64_t from = __shfl(kind ? va : ka, r) + (g0 ^ (attn_swz<GR>(i * PR) * 16));
+            attn_copy16(to + kind * H::TILE + i * 1024, (there >> r) & 1u ? (const void*)(uintptr_t)from : attn_zeros);
+          }
       }
       return there;
+    };
+    Core core;
+    typename Core::U q[Core::NU];  // of the next tile's pair
+    const int r = lane & 15;
+    const auto head = [&](const StepTile& t) { return t.kh * p.group + (t.unit - t.kh * w.blocks) * kDecodeHeads; };
+    const auto heads = [&](const StepTile& t) { return min(kDecodeHeads, (t.kh + 1) * p.group - head(t)); };
+    const auto query = [&](const StepTile& t) {
+      core.load(q, (const char*)p.q + t.seq * p.q_st + (head(t) + r) * p.q_sh, r < heads(t), lane);
     };
 
     StepTile now = x, then = x;
     uint32_t there, there_then = 0;
     ask(x, true, 0);
+    query(x);
     attn_wait<0>();
     there = fetch(now, true, 0, 0);
     if (a + 1 < b) w.next(x, lane);
     then = x;
     ask(x, a + 1 < b, 1);
-    AttnCore<TI, D, TT> core;
     bool fresh = true;
     for (int64_t t = a; t < b; ++t) {
       const int stage = (int)(t - a) & 1;
-      // entries of the tile after the next
-      if (t + 2 < b) w.next(x, lane);
+      attn_wait<0>();  // this tile, the next one's entries, a new pair's queries
       attn_wait_lds();
-      ask(x, t + 2 < b, stage);
-      attn_wait<1>();  // this tile, and the next one's entries
-      there_then = fetch(then, t + 1 < b, stage ^ 1, stage ^ 1);
-      const int kh = now.unit / w.blocks, h0 = kh * p.group + (now.unit - kh * w.blocks) * kDecodeHeads;
-      const int heads = min(kDecodeHeads, (kh + 1) * p.group - h0);
-      const int r = lane & 15;
       if (fresh) {
         core.reset();
-        core.load((const char*)p.q + now.seq * p.q_st + (h0 + r) * p.q_sh, r < heads, lane);
+#pragma unroll
+        for (int u = 0; u < Core::NU; ++u) core.q[u] = q[u];
         fresh = false;
       }
+      // entries of the tile after the next
+      if (t + 2 < b) w.next(x, lane);
+      ask(x, t + 2 < b, stage);
+      if (now.tile + 1 == now.tiles && t + 1 < b) query(then);
+      there_then = fetch(then, t + 1 < b, stage ^ 1, stage ^ 1);
       f32x4 s[TT];
       core.scores(ring + 2 * stage * H::TILE, s, lane);
 #pragma unroll
@@ -469,14 +507,15 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
       core.add(ring + (2 * stage + 1) * H::TILE, s, lane);
       if (now.tile + 1 == now.tiles || t + 1 == b) {
         fresh = true;
-        if (first >= a && now.tile + 1 == now.tiles) {
-          core.store(r < heads ? (char*)p.out + now.seq * p.o_st + (h0 + r) * p.o_sh : nullptr, lane);
+        const bool begun = first >= a;
+        if (begun && now.tile + 1 == now.tiles) {
+          core.store(r < heads(now) ? (char*)p.out + now.seq * p.o_st + (head(now) + r) * p.o_sh : nullptr, lane);
+          if (p.by_pair && lane == 0) ((int4*)p.chains)[now.seq * w.units + now.unit] = make_int4(0, 0, 0, 0);
         } else {
           // a part: of a pair begun here the second slot
-          const bool begun = first >= a;
           float* part = p.parts + (2 * (int64_t)wave + (begun ? 1 : 0)) * attn_part_floats(D);
           const float sum = core.total();
-          if (r < heads) {
+          if (r < heads(now)) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) *(f32x4*)(part + r * D + 16 * i + 4 * (lane >> 4)) = core.o[i];
             if (lane < 16) {
@@ -491,6 +530,8 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
             chain = (int)(last - wave) + 1;
             chain_seq = now.seq;
             chain_unit = now.unit;
+            if (p.by_pair && lane == 0)
+              ((int4*)p.chains)[now.seq * w.units + now.unit] = make_int4(chain, chain_seq, chain_unit, wave);
           }
         }
         first += now.tiles;
@@ -501,71 +542,108 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
     }
     attn_wait<0>();  // no copy may land after the workgroup's end
   }
-  if (lane == 0) ((int4*)p.chains)[wave] = make_int4(chain, chain_seq, chain_unit, 0);
+  if (!p.by_pair && lane == 0) ((int4*)p.chains)[wave] = make_int4(chain, chain_seq, chain_unit, wave);
   // sequences that hold nothing
   for (int64_t i = wave; i < p.n_seq; i += p.waves) {
     if (attn_len(p, (int)i) != 0) continue;
     for (int g = lane; g < p.heads * GR; g += 64)
       st16((char*)p.out + i * p.o_st + (g / GR) * p.o_sh + (g % GR) * 16, make_uint4(0u, 0u, 0u, 0u));
+    if (p.by_pair)
+      for (int u = lane; u < w.units; u += 64) ((int4*)p.chains)[i * w.units + u] = make_int4(0, 0, 0, 0);
   }
 }
 
-// Joins the parts of one wave's chain, a head a workgroup: threads of a part
-// share the head's d in fours.
-template <typename TI, int D>
-__global__ __launch_bounds__(256) void join_kernel(AttnParams p) {
-  constexpr int W = D / 4, PG = 256 / W;
-  __shared__ f32x4 s_o[256];
-  __shared__ float s_l[PG], s_m[4];
-  const int wave = blockIdx.x, r = blockIdx.y;
-  const int4 c = ((const int4*)p.chains)[wave];
-  const int n = c.x;
+// Joins the parts of the chains: 64 fours of a chain's (head, d) a wave, or
+// SPLIT waves, each with a share of the parts.
+template <typename TI, int D, int SPLIT>
+__global__ __launch_bounds__((64 * (SPLIT > 1 ? SPLIT : 4))) void join_kernel(AttnParams p) {
+  constexpr int W = D / 4, BATCH = 8;
+  __shared__ f32x4 s_o[SPLIT > 1 ? SPLIT * 64 : 1];
+  __shared__ float s_m[SPLIT > 1 ? SPLIT * 64 : 1], s_l[SPLIT > 1 ? SPLIT * 64 : 1];
+  const int lane = threadIdx.x & 63, sub = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int4 c = ((const int4*)p.chains)[SPLIT > 1 ? blockIdx.x : blockIdx.x * 4 + sub];
+  const int n = __builtin_amdgcn_readfirstlane(c.x), wave = __builtin_amdgcn_readfirstlane(c.w);
   if (n == 0) return;
   const int blocks = (p.group + kDecodeHeads - 1) / kDecodeHeads;
-  const int kh = c.z / blocks, h = kh * p.group + (c.z - kh * blocks) * kDecodeHeads + r;
-  if (h >= (kh + 1) * p.group) return;
-  const int tid = threadIdx.x, g = tid / W, x = tid % W;
-  // part 0 is the wave's second slot, the others are the next waves' first
-  const auto part = [&](int i) { return p.parts + (2 * (int64_t)(wave + i) + (i == 0 ? 1 : 0)) * attn_part_floats(D); };
-  float m = -INFINITY;
-  for (int i = tid; i < n; i += 256) m = fmaxf(m, part(i)[16 * D + r]);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  if ((tid & 63) == 0) s_m[tid >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  if (m == -INFINITY) m = 0.f;  // (no part sees anything)
+  const int kh = blocks == 1 ? c.z : c.z / blocks, h0 = kh * p.group + (c.z - kh * blocks) * kDecodeHeads;
+  const int heads = min(kDecodeHeads, (kh + 1) * p.group - h0);
+  const int r = (blockIdx.y * 64 + lane) / W, x = lane % W;
+  const int rr = min(r, heads - 1);
+  float m = -INFINITY, l = 0.f;
   f32x4 o = zero4();
-  float l = 0.f;
-  for (int i = g; i < n; i += PG) {
-    const float* q = part(i);
-    const float w = __builtin_amdgcn_exp2f(q[16 * D + r] - m);
-    const f32x4 v = *(const f32x4*)(q + r * D + 4 * x);
-    l += w * q[16 * D + 16 + r];
+  for (int i0 = SPLIT > 1 ? sub : 0; i0 < n; i0 += SPLIT * BATCH) {
+    float pm[BATCH], pl[BATCH];
+    f32x4 po[BATCH];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += w * v[e];
-  }
-  s_o[tid] = o;
-  if (x == 0) s_l[g] = l;
-  __syncthreads();
-  if (g == 0) {
-    for (int k = 1; k < PG; ++k) {
-      l += s_l[k];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] += s_o[k * W + x][e];
+    for (int k = 0; k < BATCH; ++k) {
+      // part 0 is the wave's second slot, the others are the next waves' first
+      const int i = min(i0 + k * SPLIT, n - 1);
+      const float* part = p.parts + (2 * (int64_t)(wave + i) + (i == 0 ? 1 : 0)) * attn_part_floats(D);
+      pm[k] = part[16 * D + rr];
+      pl[k] = part[16 * D + 16 + rr];
+      po[k] = *(const f32x4*)(part + rr * D + 4 * x);
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    store4<TI>((TI*)((char*)p.out + c.y * p.o_st + h * p.o_sh) + 4 * x, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      pm[k] = i0 + k * SPLIT < n ? pm[k] : -INFINITY;
+      pl[k] = i0 + k * SPLIT < n ? pl[k] : 0.f;
+      top = fmaxf(top, pm[k]);
+    }
+    const float from = top == -INFINITY ? 0.f : top, keep = __builtin_amdgcn_exp2f(m - from);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= keep;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float f = __builtin_amdgcn_exp2f(pm[k] - from);
+      l += f * pl[k];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += i0 + k * SPLIT < n ? f * po[k][e] : 0.f;
+    }
   }
+  if constexpr (SPLIT > 1) {
+    s_o[threadIdx.x] = o;
+    s_m[threadIdx.x] = m;
+    s_l[threadIdx.x] = l;
+    __syncthreads();
+    if (sub != 0) return;
+    const int k1 = min(n, SPLIT);
+    for (int k = 1; k < k1; ++k) m = fmaxf(m, s_m[k * 64 + lane]);
+    const float from = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+    o = zero4();
+    for (int k = 0; k < k1; ++k) {
+      const float f = __builtin_amdgcn_exp2f(s_m[k * 64 + lane] - from);
+      l += f * s_l[k * 64 + lane];
+      const f32x4 v = s_o[k * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += f * v[e];
+    }
+  }
+  if (r >= heads) return;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  store4<TI>((TI*)((char*)p.out + c.y * p.o_st + (h0 + r) * p.o_sh) + 4 * x, o[0] * inv, o[1] * inv, o[2] * inv,
+             o[3] * inv);
 }
 
+// Few pairs make long chains, which 16 waves share; of many most are short.
 template <typename TI, int D>
-hipError_t launch_step(const AttnParams& p, hipStream_t s) {
+hipError_t launch_step(AttnParams p, hipStream_t s) {
   using H = StepShape<TI, D>;
+  const int heads = std::min(p.group, kDecodeHeads);
+  const int64_t pairs = (int64_t)p.n_seq * p.kv * ((p.group + kDecodeHeads - 1) / kDecodeHeads);
+  const unsigned chunks = (unsigned)(heads * (D / 4) + 63) / 64;
+  p.by_pair = pairs <= p.waves / 4;
+  p.waves_log2 = __builtin_ctz(p.waves);
   hipLaunchKernelGGL((step_kernel<TI, D>), dim3(p.waves / H::NW), dim3(64 * H::NW), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((join_kernel<TI, D>), dim3(p.waves, std::min(p.group, kDecodeHeads)), dim3(256), 0, s, p);
+  if (p.by_pair)
+    hipLaunchKernelGGL((join_kernel<TI, D, 16>), dim3((unsigned)pairs, chunks), dim3(1024), 0, s, p);
+  else
+    hipLaunchKernelGGL((join_kernel<TI, D, 1>), dim3(p.waves / 4, chunks), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -639,7 +717,7 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
   char* const out = mine < t.n ? (char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh : nullptr;
   AttnCore<TI, D, TT> core;
   core.reset();
-  core.load((const char*)p.q + (int64_t)(t.row + mine) * p.q_st + h * p.q_sh, mine < t.n, lane);
+  core.load(core.q, (const char*)p.q + (int64_t)(t.row + mine) * p.q_st + h * p.q_sh, mine < t.n, lane);
 
   // key tiles: those of the sinks, then those from the window's start on
   const int end = hi / TK + (hi >= 0 ? 1 : 0);
