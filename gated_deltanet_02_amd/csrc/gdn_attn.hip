@@ -307,8 +307,7 @@ struct StepWork {
     x.unit = unit;
     x.kh = blocks == 1 ? unit : unit / blocks;
   }
-  __device__ __forceinline__ void enter(StepTile& x, int seq) const {
-    const int len = attn_len(p, seq);
+  __device__ __forceinline__ void enter(StepTile& x, int seq, int len) const {
     x.seq = seq;
     x.len = len;
     x.low = p.window > 0 ? len - 1 - p.window : -1;
@@ -331,7 +330,8 @@ struct StepWork {
       while ((some = __ballot(lane_len((int64_t)seq + lane) > 0)) == 0) seq += 64;
       seq += __ffsll((unsigned long long)some) - 1;
     }
-    enter(x, __builtin_amdgcn_readfirstlane(seq));
+    seq = __builtin_amdgcn_readfirstlane(seq);
+    enter(x, seq, attn_len(p, seq));
   }
 };
 
@@ -369,12 +369,14 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
   // [l c, (l + 1) c), c a 64th of all
   const int64_t c = ((int64_t)p.n_seq + 63) / 64;
   int64_t sum = 0;
+  int mine_len = 0;  // (the lane's only one's)
   for (int64_t i = lane * c; i < (lane + 1) * c; i += 8) {
     int len[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) len[k] = w.lane_len(i + k);
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum += i + k < (lane + 1) * c ? w.tiles(len[k]) : 0;
+    mine_len = len[0];
   }
   const int64_t upto = wave_upto(sum, lane);
   const int64_t all = wave_pick(upto, 63) * w.units;
@@ -405,7 +407,8 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
         before += wave_pick(inner - mine, k);
         i0 += k;
       }
-      w.enter(x, __builtin_amdgcn_readfirstlane((int)i0));
+      const int seq = __builtin_amdgcn_readfirstlane((int)i0);
+      w.enter(x, seq, c > 1 ? attn_len(p, seq) : __builtin_amdgcn_readlane(mine_len, at));
       const int64_t rest = a - before * w.units;
       const int unit = rest >> 31 ? (int)(rest / x.tiles) : (int)((uint32_t)rest / (uint32_t)x.tiles);
       w.turn(x, __builtin_amdgcn_readfirstlane(unit));
@@ -553,97 +556,127 @@ __global__ __launch_bounds__((64 * StepShape<TI, D>::NW)) void step_kernel(AttnP
   }
 }
 
-// Joins the parts of the chains: 64 fours of a chain's (head, d) a wave, or
-// SPLIT waves, each with a share of the parts.
-template <typename TI, int D, int SPLIT>
-__global__ __launch_bounds__((64 * (SPLIT > 1 ? SPLIT : 4))) void join_kernel(AttnParams p) {
+// Joins the parts of the chains, PER of them a workgroup of WAVES waves: a lane
+// takes four elements of a head.  A chain of at most kShortChain parts is one
+// wave's, a longer one all waves', each with every WAVES-th part.
+constexpr int kShortChain = 32;
+
+template <typename TI, int D, int WAVES, int PER>
+__global__ __launch_bounds__((64 * WAVES)) void join_kernel(AttnParams p) {
   constexpr int W = D / 4, BATCH = 8;
-  __shared__ f32x4 s_o[SPLIT > 1 ? SPLIT * 64 : 1];
-  __shared__ float s_m[SPLIT > 1 ? SPLIT * 64 : 1], s_l[SPLIT > 1 ? SPLIT * 64 : 1];
+  __shared__ f32x4 s_o[WAVES * 64];
+  __shared__ float s_m[WAVES * 64], s_l[WAVES * 64];
   const int lane = threadIdx.x & 63, sub = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int4 c = ((const int4*)p.chains)[SPLIT > 1 ? blockIdx.x : blockIdx.x * 4 + sub];
-  const int n = __builtin_amdgcn_readfirstlane(c.x), wave = __builtin_amdgcn_readfirstlane(c.w);
-  if (n == 0) return;
   const int blocks = (p.group + kDecodeHeads - 1) / kDecodeHeads;
-  const int kh = blocks == 1 ? c.z : c.z / blocks, h0 = kh * p.group + (c.z - kh * blocks) * kDecodeHeads;
-  const int heads = min(kDecodeHeads, (kh + 1) * p.group - h0);
   const int r = (blockIdx.y * 64 + lane) / W, x = lane % W;
-  const int rr = min(r, heads - 1);
-  float m = -INFINITY, l = 0.f;
-  f32x4 o = zero4();
-  for (int i0 = SPLIT > 1 ? sub : 0; i0 < n; i0 += SPLIT * BATCH) {
-    float pm[BATCH], pl[BATCH];
-    f32x4 po[BATCH];
+  int4 chains[PER];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      // part 0 is the wave's second slot, the others are the next waves' first
-      const int i = min(i0 + k * SPLIT, n - 1);
-      const float* part = p.parts + (2 * (int64_t)(wave + i) + (i == 0 ? 1 : 0)) * attn_part_floats(D);
-      pm[k] = part[16 * D + rr];
-      pl[k] = part[16 * D + 16 + rr];
-      po[k] = *(const f32x4*)(part + rr * D + 4 * x);
+  for (int k = 0; k < PER; ++k) chains[k] = ((const int4*)p.chains)[blockIdx.x * PER + k];
+
+  float m, l;
+  f32x4 o;
+  int heads, h0;
+  // the parts first, first + step, .. of a chain
+  const auto gather = [&](const int4& c, int first, int step) {
+    const int n = c.x, kh = blocks == 1 ? c.z : c.z / blocks;
+    h0 = kh * p.group + (c.z - kh * blocks) * kDecodeHeads;
+    heads = min(kDecodeHeads, (kh + 1) * p.group - h0);
+    const int rr = min(r, heads - 1);
+    m = -INFINITY;
+    l = 0.f;
+    o = zero4();
+    for (int i0 = first; i0 < n; i0 += step * BATCH) {
+      float pm[BATCH], pl[BATCH];
+      f32x4 po[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        // part 0 is the wave's second slot, the others are the next waves' first
+        const int i = min(i0 + k * step, n - 1);
+        const float* part = p.parts + (2 * (int64_t)(c.w + i) + (i == 0 ? 1 : 0)) * attn_part_floats(D);
+        pm[k] = part[16 * D + rr];
+        pl[k] = part[16 * D + 16 + rr];
+        po[k] = *(const f32x4*)(part + rr * D + 4 * x);
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        pm[k] = i0 + k * step < n ? pm[k] : -INFINITY;
+        pl[k] = i0 + k * step < n ? pl[k] : 0.f;
+        top = fmaxf(top, pm[k]);
+      }
+      const float from = top == -INFINITY ? 0.f : top, keep = __builtin_amdgcn_exp2f(m - from);
+      m = top;
+      l *= keep;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= keep;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const float f = __builtin_amdgcn_exp2f(pm[k] - from);
+        l += f * pl[k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += i0 + k * step < n ? f * po[k][e] : 0.f;
+      }
     }
-    float top = m;
+  };
+  const auto store = [&](const int4& c) {
+    if (r >= heads) return;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    store4<TI>((TI*)((char*)p.out + c.y * p.o_st + (h0 + r) * p.o_sh) + 4 * x, o[0] * inv, o[1] * inv, o[2] * inv,
+               o[3] * inv);
+  };
+
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      pm[k] = i0 + k * SPLIT < n ? pm[k] : -INFINITY;
-      pl[k] = i0 + k * SPLIT < n ? pl[k] : 0.f;
-      top = fmaxf(top, pm[k]);
+  for (int k = 0; k < PER; ++k)
+    if (k % WAVES == sub && chains[k].x > 0 && chains[k].x <= kShortChain) {
+      gather(chains[k], 0, 1);
+      store(chains[k]);
     }
-    const float from = top == -INFINITY ? 0.f : top, keep = __builtin_amdgcn_exp2f(m - from);
-    m = top;
-    l *= keep;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] *= keep;
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const float f = __builtin_amdgcn_exp2f(pm[k] - from);
-      l += f * pl[k];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] += i0 + k * SPLIT < n ? f * po[k][e] : 0.f;
-    }
-  }
-  if constexpr (SPLIT > 1) {
+  for (int k = 0; k < PER; ++k) {
+    if (chains[k].x <= kShortChain) continue;
+    gather(chains[k], sub, WAVES);
     s_o[threadIdx.x] = o;
     s_m[threadIdx.x] = m;
     s_l[threadIdx.x] = l;
     __syncthreads();
-    if (sub != 0) return;
-    const int k1 = min(n, SPLIT);
-    for (int k = 1; k < k1; ++k) m = fmaxf(m, s_m[k * 64 + lane]);
-    const float from = m == -INFINITY ? 0.f : m;
-    l = 0.f;
-    o = zero4();
-    for (int k = 0; k < k1; ++k) {
-      const float f = __builtin_amdgcn_exp2f(s_m[k * 64 + lane] - from);
-      l += f * s_l[k * 64 + lane];
-      const f32x4 v = s_o[k * 64 + lane];
+    if (sub == 0) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] += f * v[e];
+      for (int i = 1; i < WAVES; ++i) m = fmaxf(m, s_m[i * 64 + lane]);
+      const float from = m == -INFINITY ? 0.f : m;
+      l = 0.f;
+      o = zero4();
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) {
+        const float f = __builtin_amdgcn_exp2f(s_m[i * 64 + lane] - from);
+        l += f * s_l[i * 64 + lane];
+        const f32x4 v = s_o[i * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += f * v[e];
+      }
+      store(chains[k]);
     }
+    __syncthreads();
   }
-  if (r >= heads) return;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  store4<TI>((TI*)((char*)p.out + c.y * p.o_st + (h0 + r) * p.o_sh) + 4 * x, o[0] * inv, o[1] * inv, o[2] * inv,
-             o[3] * inv);
 }
 
-// Few pairs make long chains, which 16 waves share; of many most are short.
+// Few pairs make long chains, and each has a large workgroup; of many most are
+// short (64 sequences x 8 heads with a window of 1024, some four parts each: 52
+// us in all, with a large workgroup each 56).
 template <typename TI, int D>
 hipError_t launch_step(AttnParams p, hipStream_t s) {
   using H = StepShape<TI, D>;
   const int heads = std::min(p.group, kDecodeHeads);
   const int64_t pairs = (int64_t)p.n_seq * p.kv * ((p.group + kDecodeHeads - 1) / kDecodeHeads);
   const unsigned chunks = (unsigned)(heads * (D / 4) + 63) / 64;
-  p.by_pair = pairs <= p.waves / 4;
+  p.by_pair = pairs <= p.waves / 16;
   p.waves_log2 = __builtin_ctz(p.waves);
   hipLaunchKernelGGL((step_kernel<TI, D>), dim3(p.waves / H::NW), dim3(64 * H::NW), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.by_pair)
-    hipLaunchKernelGGL((join_kernel<TI, D, 16>), dim3((unsigned)pairs, chunks), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL((join_kernel<TI, D, 16, 1>), dim3((unsigned)pairs, chunks), dim3(1024), 0, s, p);
   else
-    hipLaunchKernelGGL((join_kernel<TI, D, 1>), dim3(p.waves / 4, chunks), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((join_kernel<TI, D, 4, 4>), dim3(p.waves / 4, chunks), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -302,3 +302,12 @@ def test_prefill_around_the_split(d, lengths, H):
 @pytest.mark.parametrize("lengths", [[8193], [2048, 17, 900]])
 def test_prefill_window_around_the_split(lengths):
     prefill(72, lengths, 4, 2, 128, torch.bfloat16, window=130, sinks=70)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, torch.bfloat16), (128, torch.bfloat16), (256, torch.bfloat16), (128, torch.float32)])
+@pytest.mark.parametrize("n", [1, 3, 16, 40, 200])
+def test_decode_one_long_among_short(d, dtype, n):
+    """Chains of one part, of a few and of hundreds, joined by one wave or by all."""
+    lens = [3 + 7 * i % 90 for i in range(n)]
+    lens[n // 2] = 30000
+    decode(73, lens, 6, 2, d, dtype, 16)
