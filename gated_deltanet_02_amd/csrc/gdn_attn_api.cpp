@@ -155,25 +155,31 @@ int check_rows_of(const gdn_tensor* q, const gdn_tensor* out, int lo, int hi) {
   return GDN_OK;
 }
 
+// The bytes of a stride that is taken, else 0 (of one row it may be anything).
+int64_t step(const gdn_tensor* t, int i) {
+  return !is_empty(t) && t->shape[i] > 1 ? t->stride[i] * element_size(t->dtype) : 0;
+}
+
 void fill(const Attn& A, const gdn_tensor* q, const gdn_tensor* k, const gdn_tensor* v, const gdn_tensor* table,
           const gdn_tensor* lens, const gdn_tensor* out, AttnParams* p) {
-  const int64_t es = element_size(q->dtype);
   const int r = q->ndim, c = k->ndim;
   p->q = q->data;
   p->k = k->data;
   p->v = v->data;
   p->out = out->data;
-  p->q_sh = q->stride[r - 2] * es;
-  p->o_sh = out->stride[r - 2] * es;
-  p->k_st = k->stride[c - 3] * es;
-  p->k_sh = k->stride[c - 2] * es;
-  p->v_st = v->stride[c - 3] * es;
-  p->v_sh = v->stride[c - 2] * es;
+  p->q_sh = step(q, r - 2);
+  p->o_sh = step(out, r - 2);
+  p->k_st = step(k, c - 3);
+  p->k_sh = step(k, c - 2);
+  p->v_st = step(v, c - 3);
+  p->v_sh = step(v, c - 2);
   if (table) {
-    p->k_sp = k->stride[0] * es;
-    p->v_sp = v->stride[0] * es;
-    p->table = (const int32_t*)table->data;
-    p->table_st = table->stride[0];
+    p->k_sp = step(k, 0);
+    p->v_sp = step(v, 0);
+    // (a table of no pages may have no address; none of it is read then, but
+    // that there is one tells the caches from rows)
+    p->table = (const int32_t*)(table->data ? table->data : lens->data);
+    p->table_st = step(table, 0) / 4;
     p->lens = (const int32_t*)lens->data;
     p->width = (int32_t)A.width;
     p->pages = (int32_t)A.pages;
@@ -239,7 +245,7 @@ int gdn_cache_plan(const gdn_tensor* ctx_lens, const gdn_tensor* cu_seqlens, gdn
   p.cu = cu_seqlens ? cu_seqlens->data : nullptr;
   p.cu_i64 = cu_seqlens && cu_seqlens->dtype == GDN_DTYPE_I64;
   p.table = (int32_t*)block_table->data;
-  p.table_st = block_table->stride[0];
+  p.table_st = step(block_table, 0) / 4;
   p.free = (const int32_t*)free_pages->data;
   p.free_max = (int32_t)free_pages->shape[0];
   p.n_free = (const int32_t*)n_free->data;
@@ -277,7 +283,7 @@ int gdn_cache_release(const gdn_tensor* done, gdn_tensor* seq_lens, gdn_tensor* 
   p.done = (const int32_t*)done->data;
   p.lens = (int32_t*)seq_lens->data;
   p.table = (int32_t*)block_table->data;
-  p.table_st = block_table->stride[0];
+  p.table_st = step(block_table, 0) / 4;
   p.free = (int32_t*)free_pages->data;
   p.n_free = (int32_t*)n_free->data;
   p.n = (int32_t)n;
@@ -322,27 +328,26 @@ int gdn_cache_store(const gdn_tensor* k, const gdn_tensor* v, const gdn_tensor* 
     return api_fail(GDN_ERR_LAYOUT, "k_cache overlaps v_cache");
   api_clear_error();
   if (t == 0 || is_empty(k_cache)) return GDN_OK;
-  const int64_t es = element_size(k->dtype);
   StoreParams p{};
   p.k = k->data;
   p.v = v->data;
   p.k_cache = k_cache->data;
   p.v_cache = v_cache->data;
   p.slots = (const int64_t*)slots->data;
-  p.k_st = k->stride[0] * es;
-  p.k_sh = k->stride[1] * es;
-  p.v_st = v->stride[0] * es;
-  p.v_sh = v->stride[1] * es;
-  p.kc_sp = k_cache->stride[0] * es;
-  p.kc_st = k_cache->stride[1] * es;
-  p.kc_sh = k_cache->stride[2] * es;
-  p.vc_sp = v_cache->stride[0] * es;
-  p.vc_st = v_cache->stride[1] * es;
-  p.vc_sh = v_cache->stride[2] * es;
+  p.k_st = step(k, 0);
+  p.k_sh = step(k, 1);
+  p.v_st = step(v, 0);
+  p.v_sh = step(v, 1);
+  p.kc_sp = step(k_cache, 0);
+  p.kc_st = step(k_cache, 1);
+  p.kc_sh = step(k_cache, 2);
+  p.vc_sp = step(v_cache, 0);
+  p.vc_st = step(v_cache, 1);
+  p.vc_sh = step(v_cache, 2);
   p.n_slots = k_cache->shape[0] * k_cache->shape[1];
   p.t = (int32_t)t;
   p.kv = (int32_t)kv;
-  for (p.row_shift = 0; (16 << p.row_shift) < d * es;) ++p.row_shift;
+  for (p.row_shift = 0; (16 << p.row_shift) < d * element_size(k->dtype);) ++p.row_shift;
   p.page = divide_by((uint32_t)k_cache->shape[1]);
   const hipError_t e = launch_cache_store(p, (hipStream_t)stream);
   if (e != hipSuccess) return api_fail(GDN_ERR_HIP, "cache store launch: %s", hipGetErrorString(e));
@@ -401,11 +406,11 @@ int gdn_attn_prefill(const gdn_tensor* q, const gdn_tensor* k, const gdn_tensor*
   AttnParams p{};
   fill(A, q, k, v, block_table, seq_lens, out, &p);
   const int64_t es = element_size(q->dtype);
-  p.q_st = tq.st * es;
-  p.o_st = to.st * es;
+  p.q_st = A.T > 1 ? tq.st * es : 0;
+  p.o_st = A.T > 1 ? to.st * es : 0;
   if (!block_table) {
-    p.k_st = tk.st * es;
-    p.v_st = tv.st * es;
+    p.k_st = A.T > 1 ? tk.st * es : 0;
+    p.v_st = A.T > 1 ? tv.st * es : 0;
   }
   p.cu = cu_seqlens ? cu_seqlens->data : nullptr;
   p.cu_i64 = cu_seqlens && cu_seqlens->dtype == GDN_DTYPE_I64;
@@ -458,9 +463,8 @@ int gdn_attn_decode(const gdn_tensor* q, const gdn_tensor* k_cache, const gdn_te
   if (n == 0) return GDN_OK;
   AttnParams p{};
   fill(A, q, k_cache, v_cache, block_table, seq_lens, out, &p);
-  const int64_t es = element_size(q->dtype);
-  p.q_st = q->stride[0] * es;
-  p.o_st = out->stride[0] * es;
+  p.q_st = step(q, 0);
+  p.o_st = step(out, 0);
   p.n_seq = (int32_t)n;
   p.t_total = (int32_t)n;
   p.waves = attn_decode_waves(bf16, (int)A.D);
