@@ -27,10 +27,7 @@ constexpr int kPlanTokens = 2048;  // of a workgroup
 __device__ __forceinline__ int quotient(const Divide& d, int n) {
   return (int)((__umulhi(d.mul, (uint32_t)n) + (uint32_t)n) >> d.shift);
 }
-__device__ __forceinline__ int quotient_up(const Divide& d, int64_t n) {
-  // (n may be up to 2^32: a length and new tokens)
-  return (int)(((uint64_t)n + d.d - 1) / d.d);
-}
+__device__ __forceinline__ int quotient_up(const Divide& d, int n) { return n > 0 ? quotient(d, n - 1) + 1 : 0; }
 
 __device__ __forceinline__ int cu_at(const void* cu, int i64, int64_t i, int t) {
   const int64_t v = i64 ? ((const int64_t*)cu)[i] : (int64_t)((const int32_t*)cu)[i];
@@ -56,7 +53,7 @@ __device__ __forceinline__ Request request(const PlanParams& p, int i) {
   }
   r.have = quotient_up(p.page, r.ctx);
   const int64_t end = (int64_t)r.ctx + r.fresh;
-  const int need = quotient_up(p.page, end);
+  const int need = quotient_up(p.page, (int)min(end, (int64_t)INT32_MAX));
   r.fits = need <= p.width && end <= INT32_MAX;
   r.extra = r.fits ? need - r.have : 0;
   return r;
@@ -106,8 +103,8 @@ __device__ __forceinline__ void plan_finish(const PlanParams& p, int c, int64_t 
   if (threadIdx.x == 0) p.n_free_out[0] = (int)n_free - taken;
 }
 
-// FINISH: one workgroup that also writes the lengths (which may be the ones
-// read) once all its reads are done.
+// FINISH: the first workgroup also writes the lengths, once all its reads are
+// done; where they are the ones read, it is the only one.
 template <bool FINISH>
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanParams p) {
   __shared__ int64_t before[kPlanThreads], waves[kPlanThreads / 64];
@@ -158,6 +155,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanParams p) {
     p.slots[t] = slot;
   }
   if constexpr (FINISH) {
+    if (blockIdx.x > 0) return;
     __syncthreads();
     plan_finish(p, c, mine, n_free);
   }
@@ -211,12 +209,12 @@ __global__ __launch_bounds__(kPlanThreads) void release_kernel(ReleaseParams p) 
 
 hipError_t launch_cache_plan(const PlanParams& p, hipStream_t s) {
   const int64_t groups = ((int64_t)p.t + kPlanTokens - 1) / kPlanTokens;
-  if (groups <= 1) {
-    hipLaunchKernelGGL(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, s, p);
+  if (groups <= 1 || (p.lens != p.ctx && p.n_free_out != p.n_free)) {
+    hipLaunchKernelGGL(plan_kernel<true>, dim3((unsigned)std::max<int64_t>(groups, 1)), dim3(kPlanThreads), 0, s, p);
     return hipGetLastError();
   }
-  // the lengths, which may be the ones that every workgroup reads, in a launch
-  // of their own
+  // lengths or a count that every workgroup reads are written in a launch of
+  // their own
   hipLaunchKernelGGL(plan_kernel<false>, dim3((unsigned)groups), dim3(kPlanThreads), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -237,7 +235,7 @@ __global__ __launch_bounds__(256) void store_kernel(StoreParams p, int64_t first
   const int64_t t = first + blockIdx.x;
   const int64_t slot = p.slots[t];
   if (slot < 0 || slot >= p.n_slots) return;
-  const int64_t page = slot / p.page.d, in = slot - page * p.page.d;
+  const int64_t page = slot <= INT32_MAX ? quotient(p.page, (int)slot) : slot / p.page.d, in = slot - page * p.page.d;
   const char* k = (const char*)p.k + t * p.k_st;
   const char* v = (const char*)p.v + t * p.v_st;
   char* kc = (char*)p.k_cache + page * p.kc_sp + in * p.kc_st;
