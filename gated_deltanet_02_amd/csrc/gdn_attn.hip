@@ -681,15 +681,20 @@ hipError_t launch_step(AttnParams p, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// prompts, 64 queries a workgroup: 16 a wave, tiles of 32 keys shared
+// prompts, f32: 16 queries a wave.  Either four waves share tiles of 32 keys for
+// 64 queries, or (SPLIT) they share 16 queries, each with every fourth tile.
+// Bound by fp32 matrix instructions: 4096 tokens x 16 heads 101 TFLOP/s with d =
+// 128, 96 with 64 and 99 with 256 (a product of 8192^3: 153).
 
-template <typename TI, int D>
+template <typename TI, int D, bool SPLIT>
 struct TileShape {
-  static constexpr int TT = 2, TK = 32, NW = 4, ROWS = 64;
+  static constexpr int TT = SPLIT && D >= 128 ? 1 : 2, TK = 16 * TT, NW = 4, ROWS = SPLIT ? 16 : 64;
   static constexpr int RB = D * (int)sizeof(TI), GR = RB / 16, TILE = TK * RB;
-  static constexpr int PIECES = TK * GR / 64 / NW;  // copies of a tile, a wave
-  static constexpr int entries = 4 * TILE, total = entries + NW * 2 * 256;
-  static_assert(PIECES >= 1 && total <= 163840, "LDS");
+  static constexpr int SHARE = SPLIT ? 1 : NW;         // waves that copy a tile
+  static constexpr int PIECES = TK * GR / 64 / SHARE;  // copies of a tile, a wave
+  static constexpr int ring = 4 * TILE, entries = NW / SHARE * ring, total = entries + NW * 2 * 256;
+  static constexpr int box = D * 64, join = NW * (box + 512);  // of a wave: O, m and l
+  static_assert(PIECES >= 1 && total <= 163840 && (!SPLIT || join <= total), "LDS");
 };
 
 // Where a workgroup's queries lie: rows [row, row + n) of q, at the places
@@ -735,31 +740,40 @@ __device__ __forceinline__ bool tile_rows(const AttnParams& p, int64_t i, int ro
   return true;
 }
 
-template <typename TI, int D, bool PAGED>
-__global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
-  using H = TileShape<TI, D>;
-  constexpr int TT = H::TT, TK = H::TK, RB = H::RB, GR = H::GR, P = H::PIECES;
+template <typename TI, int D, bool PAGED, bool SPLIT>
+__global__ __launch_bounds__(256) void tile_kernel(AttnParams p, int tiles) {
+  using H = TileShape<TI, D, SPLIT>;
+  constexpr int TT = H::TT, TK = H::TK, GR = H::GR, P = H::PIECES, NW = H::NW;
+  constexpr uint32_t ALL = TK == 32 ? 0xffffffffu : 0xffffu;
   __shared__ __attribute__((aligned(1024))) char smem[H::total];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int64_t item = blockIdx.x / p.heads;
-  const int h = blockIdx.x - (int)item * p.heads, kh = h / p.group;
+  const int item = blockIdx.x / p.heads;  // (long tiles first)
+  const int h = blockIdx.x - item * p.heads, kh = h / p.group;
   TileRows t;
-  if (!tile_rows(p, item, H::ROWS, t)) return;
+  if (!tile_rows(p, tiles - 1 - item, H::ROWS, t)) return;
   const int lo = t.place, hi = t.place + t.n - 1;  // the queries' places
-  const int mine = wave * 16 + (lane & 15), place = lo + mine;
-  char* const out = mine < t.n ? (char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh : nullptr;
+  const int skip = SPLIT ? 0 : wave * 16;          // to the wave's first query
+  const int mine = skip + (lane & 15), place = lo + mine, wave_lo = lo + skip;
   AttnCore<TI, D, TT> core;
   core.reset();
   core.load(core.q, (const char*)p.q + (int64_t)(t.row + mine) * p.q_st + h * p.q_sh, mine < t.n, lane);
 
-  // key tiles: those of the sinks, then those from the window's start on
+  // key tiles: those of the sinks, then those from the window's start on; a
+  // wave's are every SHARE-th or, split, every NW-th
   const int end = hi / TK + (hi >= 0 ? 1 : 0);
   const int from = p.window > 0 ? max(0, max(lo, 0) - p.window + 1) / TK : 0;
-  const int sinks = p.window > 0 ? (min(p.sinks, hi + 1) + TK - 1) / TK : 0;
-  const auto after = [&](int k) { return k + 1 >= sinks && k + 1 < from ? from : k + 1; };
-  const uint32_t ring_at = attn_lds(smem), entries_at = attn_lds(smem + H::entries + wave * 512);
+  const int sinks = p.window > 0 ? min((min(p.sinks, hi + 1) + TK - 1) / TK, from) : 0;
+  const int all = max(0, sinks + end - from);
+  const int turns = SPLIT ? (all - wave + NW - 1) / NW : all;
+  const auto tile_at = [&](int j) {  // `end` or more: none
+    const int i = SPLIT ? j * NW + wave : j;
+    return i < sinks ? i : from + i - sinks;
+  };
+  char* const ring = smem + (SPLIT ? wave * H::ring : 0);
+  const uint32_t ring_at = attn_lds(ring), entries_at = attn_lds(smem + H::entries + wave * 512);
   const int* entries = (const int*)(smem + H::entries + wave * 512);
-  const auto live = [&](int j) { return j <= hi && (p.window <= 0 || j > max(lo, 0) - p.window || j < p.sinks); };
+  const int low = p.window > 0 ? max(lo, 0) - p.window : -1;  // the last key before every window
+  const auto live = [&](int j) { return j <= hi && (j > low || j < p.sinks); };
   const auto ask = [&](int k, int row) {
     if (!PAGED) return;
     const int j = k * TK + lane;
@@ -767,73 +781,139 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
     if (k < end && lane < TK && live(j)) a = p.table + t.seq * p.table_st + attn_quotient(p.page, j);
     attn_copy4(entries_at + row * 256, a);
   };
+  // (as the single tokens' copies)
+  constexpr int PR = 64 / GR;
+  const bool even = !PAGED || p.page.d % PR == 0;
+  const uint32_t k_row = lane / GR * (uint32_t)p.k_st, v_row = lane / GR * (uint32_t)p.v_st;
   const auto fetch = [&](int k, int row, int stage) -> uint32_t {
     const int j = k * TK + lane;
     bool there = k < end && lane < TK && live(j);
     int page = 0, in = j;
-    if (PAGED && there) {
-      page = entries[row * 64 + lane];
-      there = (uint32_t)page < (uint32_t)p.pages;
+    if (PAGED) {
+      page = entries[row * 64 + lane % TK];
+      there = there && (uint32_t)page < (uint32_t)p.pages;
       in = j - attn_quotient(p.page, j) * (int)p.page.d;
+    } else {
+      in += t.start;
     }
-    if (!PAGED) in += t.start;
     const uint32_t mask = (uint32_t)__ballot(there);
+    uint64_t ka = (uint64_t)(uintptr_t)p.k + kh * p.k_sh + in * p.k_st;
+    uint64_t va = (uint64_t)(uintptr_t)p.v + kh * p.v_sh + in * p.v_st;
+    if (PAGED) ka += page * p.k_sp, va += page * p.v_sp;
+    const int first = SPLIT ? 0 : wave * PR;
+    constexpr int STEP = H::SHARE * PR;
+    const uint32_t to = ring_at + 2 * stage * H::TILE + (SPLIT ? 0 : wave * 1024);
+    if (even && mask == ALL) {
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const char* base = kind ? (const char*)p.v + kh * p.v_sh : (const char*)p.k + kh * p.k_sh;
-      const int64_t sp = kind ? p.v_sp : p.k_sp, st = kind ? p.v_st : p.k_st;
+      for (int kind = 0; kind < 2; ++kind)
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int piece = i * H::NW + wave, r = piece * (64 / GR) + lane / GR;
-        const int pl = __shfl(in, r);
-        int64_t o = pl * st;
-        if (PAGED) o += __shfl(page, r) * sp;
-        const char* a = base + o + (((lane % GR) ^ attn_swz<GR>(r)) * 16);
-        attn_copy16(ring_at + (2 * stage + kind) * H::TILE + piece * 1024,
-                    (mask >> r) & 1u ? a : (const char*)attn_zeros);
-      }
+        for (int i = 0; i < P; ++i) {
+          const uint32_t g = ((lane % GR) ^ attn_swz<GR>(first + i * STEP + lane / GR)) * 16;
+          attn_copy16(to + kind * H::TILE + i * H::SHARE * 1024,
+                      (const void*)(uintptr_t)wave_pick(kind ? va : ka, first + i * STEP), g + (kind ? v_row : k_row));
+        }
+    } else {
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int r = first + i * STEP + lane / GR;
+          const uint64_t a = __shfl(kind ? va : ka, r) + ((lane % GR) ^ attn_swz<GR>(r)) * 16;
+          attn_copy16(to + kind * H::TILE + i * H::SHARE * 1024, (mask >> r) & 1u ? (const void*)(uintptr_t)a : attn_zeros);
+        }
     }
     return mask;
   };
-  int now = sinks > 0 ? 0 : from, then = after(now), later = after(then);
-  int stage = 0;
-  ask(now, 0);
+  ask(tile_at(0), 0);
   attn_wait<0>();
-  uint32_t there = fetch(now, 0, 0), there_then;
-  ask(then, 1);
-  while (now < end) {
+  uint32_t there = fetch(tile_at(0), 0, 0), there_then;
+  ask(tile_at(1), 1);
+  for (int j = 0; j < turns; ++j) {
+    const int stage = j & 1, j0 = tile_at(j) * TK;
     attn_wait_lds();
-    ask(later, stage);
+    ask(tile_at(j + 2), stage);
     attn_wait<PAGED ? 1 : 0>();
-    lds_barrier();
-    there_then = fetch(then, stage ^ 1, stage ^ 1);
+    if (!SPLIT) lds_barrier();
+    there_then = fetch(tile_at(j + 1), stage ^ 1, stage ^ 1);
     f32x4 s[TT];
-    core.scores(smem + 2 * stage * H::TILE, s, lane);
+    core.scores(ring + 2 * stage * H::TILE, s, lane);
 #pragma unroll
     for (int k = 0; k < TT; ++k)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int in = 16 * k + 4 * (lane >> 4) + e, j = now * TK + in;
-        const bool see = ((there >> in) & 1u) && j <= place && (p.window <= 0 || place - j < p.window || j < p.sinks);
-        s[k][e] = see ? s[k][e] * p.scale : -INFINITY;
-      }
+      for (int e = 0; e < 4; ++e) s[k][e] *= p.scale;
+    if (!(there == ALL && j0 + TK - 1 <= wave_lo &&
+          (p.window <= 0 || j0 > wave_lo + 15 - p.window || j0 + TK <= p.sinks))) {
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int in = 16 * k + 4 * (lane >> 4) + e, at = j0 + in;
+          const bool see = ((there >> in) & 1u) && at <= place && (p.window <= 0 || place - at < p.window || at < p.sinks);
+          s[k][e] = see ? s[k][e] : -INFINITY;
+        }
+    }
     core.weigh(s);
-    core.add(smem + (2 * stage + 1) * H::TILE, s, lane);
-    now = then;
-    then = later;
-    later = after(later);
+    core.add(ring + (2 * stage + 1) * H::TILE, s, lane);
     there = there_then;
-    stage ^= 1;
   }
   attn_wait<0>();  // no copy may land after the workgroup's end
-  core.store(out, lane);
+  char* const out = mine < t.n ? (char*)p.out + (int64_t)(t.row + mine) * p.o_st + h * p.o_sh : nullptr;
+  if constexpr (!SPLIT) {
+    core.store(out, lane);
+  } else {
+    // The join: each wave ends up with a quarter of d.
+    constexpr int NC = D / 16, MY = NC / NW;
+    const float l = core.total();
+    lds_barrier();
+    f32x4* const box = (f32x4*)smem;
+    float* const ml = (float*)(smem + NW * H::box);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) box[(wave * NC + i) * 64 + lane] = core.o[i];
+    ml[wave * 128 + lane] = core.m;
+    ml[wave * 128 + 64 + lane] = l;
+    lds_barrier();
+    float m = -INFINITY, sum = 0.f, f[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, ml[w * 128 + lane]);
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      f[w] = __builtin_amdgcn_exp2f(ml[w * 128 + lane] - base);
+      sum += f[w] * ml[w * 128 + 64 + lane];
+    }
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int i = 0; i < MY; ++i) {
+      f32x4 y = zero4();
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const f32x4 v = box[(w * NC + wave * MY + i) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += f[w] * v[e];
+      }
+      if (out) store4<TI>((TI*)out + 16 * (wave * MY + i) + 4 * (lane >> 4), y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
 // prompts, bf16: 32 queries a wave, tiles of 64 keys shared by four waves
 
+//
+// Bound by the matrix instructions: one prompt of 16384 tokens x 16 heads runs
+// at 1100 TFLOP/s with d = 128, 935 with 64 and 1020 with 256, where a product
+// of 16384^3 reaches 1387.  32 columns a wave give 32 x 32 x 16 products whose
+// softmax is 16 scores a lane and 32 keys; at d <= 128 two waves a SIMD cover
+// each other's softmax (a third would not fit LDS and registers).  Weights of
+// one bf16 term: off by 2^-8 of themselves at most, as the output by its own rounding.
+// Tiles of 64 keys, two stages, one barrier a tile; copies of the next tile go
+// out between this one's products.  Tried and slower: groups of waves in turns
+// by barriers, tiles of 32 keys with the next one's scores beside the softmax
+// (119 us for 98), wave priorities.
+
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// GROUPS: of four waves, which take every GROUPS-th tile of keys and join.
 template <int D, int GROUPS>
 struct PromptShape {
   static constexpr int NW = 4, ROWS = 32 * NW, TK = 64;  // NW: waves of a group
@@ -1317,14 +1397,26 @@ hipError_t launch_prompt(const AttnParams& p, hipStream_t s) {
   return launch_prompt<D, 1>(p, tiles, s);
 }
 
+template <typename TI, int D, bool SPLIT>
+hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
+  const int tiles = (int)tiles_of(p, TileShape<TI, D, SPLIT>::ROWS);
+  const dim3 grid((unsigned)((int64_t)tiles * p.heads)), threads(256);
+  if (p.table)
+    hipLaunchKernelGGL((tile_kernel<TI, D, true, SPLIT>), grid, threads, 0, s, p, tiles);
+  else
+    hipLaunchKernelGGL((tile_kernel<TI, D, false, SPLIT>), grid, threads, 0, s, p, tiles);
+  return hipGetLastError();
+}
+
 template <typename TI, int D>
 hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)(tiles_of(p, TileShape<TI, D>::ROWS) * p.heads)), threads(256);
-  if (p.table)
-    hipLaunchKernelGGL((tile_kernel<TI, D, true>), grid, threads, 0, s, p);
-  else
-    hipLaunchKernelGGL((tile_kernel<TI, D, false>), grid, threads, 0, s, p);
-  return hipGetLastError();
+  // Few workgroups: keys shared out shorten the chain of tiles.  Measured,
+  // split and not, d = 64, 8 heads: 256 tokens 9 and 18 us, 1024 26 and 57, 2048
+  // (256 workgroups) 78 and 111, 4096 266 and 259; with a window of 256, whose
+  // chains are short, 2048 40 and 25.
+  if constexpr (D <= 128)
+    if (p.window <= 0 && tiles_of(p, 64) * p.heads <= 256) return launch_tiles<TI, D, true>(p, s);
+  return launch_tiles<TI, D, false>(p, s);
 }
 
 }  // namespace

@@ -311,3 +311,11 @@ def test_decode_one_long_among_short(d, dtype, n):
     lens = [3 + 7 * i % 90 for i in range(n)]
     lens[n // 2] = 30000
     decode(73, lens, 6, 2, d, dtype, 16)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lengths,H", [([700], 4), ([17, 0, 16, 300, 15], 6), ([2049], 8), ([1700], 10)])
+@pytest.mark.parametrize("past", [False, True])
+def test_prefill_f32_around_the_split(d, lengths, H, past):
+    """Few and many workgroups: keys shared out among the waves, or queries."""
+    prefill(74, lengths, H, 2, d, torch.float32, past=[5 + 41 * i for i in range(len(lengths))] if past else None)
