@@ -1017,13 +1017,14 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
     k_off[i] = (uint32_t)row * (uint32_t)p.k_st + g;
     v_off[i] = (uint32_t)row * (uint32_t)p.v_st + g;
   }
-  // Where a tile's rows lie: the lane's key's page, and which keys there are.
+  // Where a tile's rows lie: with pages the lane's key and value, and which keys
+  // there are.
   struct Where {
-    int tile, page;
-    uint64_t there;
+    int tile;
+    uint64_t there, ka, va;
   };
   const auto look = [&](int k, int row) {
-    Where w{k, 0, 0};
+    Where w{k, 0, 0, 0};
     const int j0 = k * TK, j = j0 + lane;
     if (!PAGED && j0 + TK - 1 <= hi && (j0 > low || j0 + TK <= p.sinks)) {
       w.there = ~0ull;
@@ -1031,8 +1032,10 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
     }
     bool is = k < end && live(j);
     if (PAGED) {
-      w.page = entries[row * 64 + lane];
-      is = is && (uint32_t)w.page < (uint32_t)p.pages;
+      const int page = entries[row * 64 + lane], in = j - attn_quotient(p.page, j) * (int)p.page.d;
+      is = is && (uint32_t)page < (uint32_t)p.pages;
+      w.ka = (uint64_t)(uintptr_t)k_base + page * p.k_sp + in * p.k_st;
+      w.va = (uint64_t)(uintptr_t)v_base + page * p.v_sp + in * p.v_st;
     }
     w.there = __ballot(is);
     return w;
@@ -1052,9 +1055,7 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
     if (values) i -= P;
     const char* from;
     if (PAGED) {
-      const int r = i * STEP + wave * PR, at = w.tile * TK + r;
-      const int pg = __builtin_amdgcn_readlane(w.page, r), in = at - attn_quotient(p.page, at) * (int)p.page.d;
-      from = values ? v_base + (pg * p.v_sp + in * p.v_st) : k_base + (pg * p.k_sp + in * p.k_st);
+      from = (const char*)(uintptr_t)wave_pick(values ? w.va : w.ka, i * STEP + wave * PR);
     } else if (values) {
       from = v_now;
       v_now += v_step;
@@ -1066,24 +1067,19 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
                    values ? v_off[i % KINDS] : k_off[i % KINDS]);
   };
   const auto fetch = [&](const Where& w, uint32_t to) {
-    const int j = w.tile * TK + lane;
-    int64_t ko, vo;
-    if (PAGED) {
-      const int in = j - attn_quotient(p.page, j) * (int)p.page.d;
-      ko = w.page * p.k_sp + in * p.k_st;
-      vo = w.page * p.v_sp + in * p.v_st;
-    } else {
-      ko = (int64_t)(t.start + j) * p.k_st;
-      vo = (int64_t)(t.start + j) * p.v_st;
+    uint64_t ka = w.ka, va = w.va;
+    if (!PAGED) {
+      ka = (uint64_t)(uintptr_t)k_base + (int64_t)(t.start + w.tile * TK + lane) * p.k_st;
+      va = (uint64_t)(uintptr_t)v_base + (int64_t)(t.start + w.tile * TK + lane) * p.v_st;
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int r = i * STEP + wave * PR + lane / GR;
-      const int64_t kr = __shfl(ko, r), vr = __shfl(vo, r);
+      const uint64_t kr = __shfl(ka, r), vr = __shfl(va, r);
       const int g = ((lane % GR) ^ attn_swz<GR>(r)) * 16;
       const bool is = (w.there >> r) & 1u;
-      attn_copy16(to + i * H::NW * 1024, is ? k_base + kr + g : (const char*)attn_zeros);
-      attn_copy16(to + i * H::NW * 1024 + H::TILE, is ? v_base + vr + g : (const char*)attn_zeros);
+      attn_copy16(to + i * H::NW * 1024, is ? (const void*)(uintptr_t)(kr + g) : attn_zeros);
+      attn_copy16(to + i * H::NW * 1024 + H::TILE, is ? (const void*)(uintptr_t)(vr + g) : attn_zeros);
     }
   };
   const auto stage_at = [&](int stage) { return ring_at + 2 * stage * H::TILE + wave * 1024; };
@@ -1113,7 +1109,7 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
     lds_barrier();
     const int j0 = here.tile * TK;
     const bool plain = !PAGED && here.tile >= plain_from && here.tile < plain_to;
-    Where next{here.tile + GROUPS, 0, ~0ull};
+    Where next{here.tile + GROUPS, ~0ull, 0, 0};
     if (!plain) next = look(tile_at(j + 1), stage ^ 1);
     const bool whole = plain || (j0 + TK - 1 <= wave_lo && here.there == ~0ull &&
                                  (p.window <= 0 || j0 > wave_hi - p.window || j0 + TK <= p.sinks));
