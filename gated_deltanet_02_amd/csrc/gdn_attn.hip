@@ -69,9 +69,12 @@ __device__ __forceinline__ uint64_t attn_scalar(uint64_t v) {
          (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
 }
 
-// The same from a common address and a lane's offset to it.
+// The same from a common address and a lane's offset to it.  The address may
+// come out of a lane (v_readlane), and an access may read such a scalar five
+// wait states later at the earliest: the compiler does not count them into
+// assembly, which therefore has them itself (here and in the next one).
 __device__ __forceinline__ void attn_copy16(uint32_t lds, const void* base, uint32_t offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(attn_scalar((uint64_t)(uintptr_t)base))
                : "memory", "m0");
