@@ -718,7 +718,9 @@ void gdn_attn_default_options(gdn_attn_options* opts);
  *   block_table, seq_lens  [N, M], [N] int32, or both NULL
  *   opts        NULL for the defaults
  * d in {64, 128, 256}; unit stride in d, other strides multiples of 16 bytes;
- * tokens of k and v at most 2^24 elements apart.
+ * tokens of k and v at most 2^24 elements apart.  The last bits of a result
+ * depend on whether the call is large or small (keys are shared out between
+ * more waves where tiles are few).
  */
 int gdn_attn_prefill(const gdn_tensor* q, const gdn_tensor* k, const gdn_tensor* v,
                      const gdn_tensor* cu_seqlens, const gdn_tensor* block_table,
