@@ -140,8 +140,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanParams p, int to
         page = p.table[i * p.table_st + col];
       }
       if (r.extra > 0) {
-        int64_t upto = before[i / c];
-        for (int64_t j = i / c * c; j < i; ++j) upto += request(p, (int)j).extra;
+        int64_t upto = before[(int)i / c];
+        for (int j = (int)i / c * c; j < i; ++j) upto += request(p, j).extra;
         if (upto + r.extra > n_free) {
           page = -1;
         } else if (col >= r.have) {

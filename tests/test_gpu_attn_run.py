@@ -294,3 +294,45 @@ def test_keys_of_minus_infinity():
         for h, keys in ((0, seen), (1, list(range(200)))):
             ref = A.attention(f64(q[199:, h: h + 1]), f64(k[keys][:, h: h + 1]), f64(v[keys][:, h: h + 1]), len(keys) - 1, 0, 0, None)
             check_out(out[199:, h: h + 1], ref, torch.bfloat16, f"head {h} d {d}")
+
+
+def test_as_many_requests_as_there_may_be():
+    """2^20 requests: a token planned for each, and 70000 sequences of which
+    most are short or empty, single tokens on them."""
+    n, page = 1 << 20, 16
+    rng = np.random.default_rng(14)
+    ctx = rng.integers(0, 40, n)
+    have, need = -(-ctx // page), -(-(ctx + 1) // page)
+    extra = need - have
+    upto = np.cumsum(extra)
+    supply = int(upto[-1]) - 1000  # (the last ones get none)
+    held = np.arange(n * 3, dtype=np.int32).reshape(n, 3)
+    table = np.where(np.arange(3) < have[:, None], held, -1)
+    free = np.arange(supply, dtype=np.int32) + 5 * n
+    tab = torch.from_numpy(table).cuda()
+    lens, slots, left = G.gdn_cache_plan(i32(ctx).cuda(), page, tab, torch.from_numpy(free).cuda(), i32([supply]).cuda())
+    served = (extra == 0) | (upto <= supply)
+    pick = np.clip(supply - upto, 0, supply - 1)  # (a page each)
+    want_page = np.where(extra > 0, free[pick], table[np.arange(n), ctx // page])
+    want = np.where(served, want_page.astype(np.int64) * page + ctx % page, -1)
+    assert np.array_equal(slots.cpu().numpy(), want)
+    assert np.array_equal(lens.cpu().numpy(), np.where(served, ctx + 1, ctx))
+    assert int(left) == supply - int(upto[served & (extra > 0)].max())
+
+    N, d = 70000, 64
+    g = gen(15)
+    lens = torch.randint(0, 4, (N,), generator=g).int()
+    lens[torch.rand(N, generator=g) < 0.3] = 0
+    lens[40000], lens[N - 1] = 900, 70
+    width, pg = 4, 256
+    k, v = randn(g, N // 8, pg, 1, d), randn(g, N // 8, pg, 1, d)
+    table = torch.randint(0, N // 8, (N, width), generator=g).int()
+    q = randn(g, N, 2, d)
+    out = G.gdn_attn_decode(q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.cuda()).cpu()
+    assert not out[lens == 0].any()
+    some = torch.cat([torch.tensor([40000, N - 1]), torch.nonzero(lens > 0)[::301, 0]]).tolist()
+    kd, vd = f64(k), f64(v)
+    for i in some:
+        m = int(lens[i])
+        ref = A.attention(f64(q[i: i + 1]), A.gather(kd, table[i].tolist(), m), A.gather(vd, table[i].tolist(), m), m - 1, 0, 0, None)
+        check_out(out[i: i + 1], ref, torch.float32, f"sequence {i}", step=True)
