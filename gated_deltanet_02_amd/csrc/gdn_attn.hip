@@ -691,8 +691,9 @@ hipError_t launch_step(AttnParams p, hipStream_t s) {
 
 template <typename TI, int D, bool SPLIT>
 struct TileShape {
-  static constexpr int TT = SPLIT && D >= 128 ? 1 : 2, TK = 16 * TT, NW = 4, ROWS = SPLIT ? 16 : 64;
+  static constexpr int TT = SPLIT && D >= 128 ? 1 : 2, TK = 16 * TT, ROWS = SPLIT ? 16 : 64;
   static constexpr int RB = D * (int)sizeof(TI), GR = RB / 16, TILE = TK * RB;
+  static constexpr int NW = SPLIT && D == 256 ? 2 : 4;  // (of rings that fit)
   static constexpr int SHARE = SPLIT ? 1 : NW;         // waves that copy a tile
   static constexpr int PIECES = TK * GR / 64 / SHARE;  // copies of a tile, a wave
   static constexpr int ring = 4 * TILE, entries = NW / SHARE * ring, total = entries + NW * 2 * 256;
@@ -744,7 +745,7 @@ __device__ __forceinline__ bool tile_rows(const AttnParams& p, int64_t i, int ro
 }
 
 template <typename TI, int D, bool PAGED, bool SPLIT>
-__global__ __launch_bounds__(256) void tile_kernel(AttnParams p, int tiles) {
+__global__ __launch_bounds__((64 * TileShape<TI, D, SPLIT>::NW)) void tile_kernel(AttnParams p, int tiles) {
   using H = TileShape<TI, D, SPLIT>;
   constexpr int TT = H::TT, TK = H::TK, GR = H::GR, P = H::PIECES, NW = H::NW;
   constexpr uint32_t ALL = TK == 32 ? 0xffffffffu : 0xffffu;
@@ -864,7 +865,7 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p, int tiles) {
   if constexpr (!SPLIT) {
     core.store(out, lane);
   } else {
-    // The join: each wave ends up with a quarter of d.
+    // The join: each wave ends up with its share of d.
     constexpr int NC = D / 16, MY = NC / NW;
     const float l = core.total();
     lds_barrier();
@@ -1398,8 +1399,9 @@ hipError_t launch_prompt(const AttnParams& p, hipStream_t s) {
 
 template <typename TI, int D, bool SPLIT>
 hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
-  const int tiles = (int)tiles_of(p, TileShape<TI, D, SPLIT>::ROWS);
-  const dim3 grid((unsigned)((int64_t)tiles * p.heads)), threads(256);
+  using H = TileShape<TI, D, SPLIT>;
+  const int tiles = (int)tiles_of(p, H::ROWS);
+  const dim3 grid((unsigned)((int64_t)tiles * p.heads)), threads(64 * H::NW);
   if (p.table)
     hipLaunchKernelGGL((tile_kernel<TI, D, true, SPLIT>), grid, threads, 0, s, p, tiles);
   else
@@ -1413,8 +1415,13 @@ hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
   // split and not, d = 64, 8 heads: 256 tokens 9 and 18 us, 1024 26 and 57, 2048
   // (256 workgroups) 78 and 111, 4096 266 and 259; with a window of 256, whose
   // chains are short, 2048 40 and 25.
-  if constexpr (D <= 128)
-    if (p.window <= 0 && tiles_of(p, 64) * p.heads <= 256) return launch_tiles<TI, D, true>(p, s);
+  // Few workgroups: keys shared out shorten the chain of tiles.  Measured,
+  // split and not, d = 64, 8 heads: 256 tokens 9 and 18 us, 1024 26 and 57, 2048
+  // (256 workgroups) 78 and 111, 4096 266 and 259; with a window of 256, whose
+  // chains are short, 2048 40 and 25.  d = 256, two waves, one head: 3000 tokens
+  // 361 and 489, 8192 (128 workgroups) 1040 and 1311, two heads of that 2027 and
+  // 1313.
+  if (p.window <= 0 && tiles_of(p, 64) * p.heads <= (D == 256 ? 128 : 256)) return launch_tiles<TI, D, true>(p, s);
   return launch_tiles<TI, D, false>(p, s);
 }
 
