@@ -194,6 +194,12 @@ struct AttnCore {
 #pragma unroll
     for (int t = 0; t < TT; ++t) settle(s[t]);
   }
+  // a - b with both as they are: a score's product with the scale joined to it
+  // would leave the largest one's rounding as an exponent.
+  static __device__ __forceinline__ float minus(float a, float b) {
+#pragma clang fp contract(off)
+    return a - b;
+  }
   // Takes a tile of scores in: s becomes the weights.
   __device__ __forceinline__ void weigh(f32x4 (&s)[TT]) {
     float top = s[0][0];
@@ -213,7 +219,7 @@ struct AttnCore {
     for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[t][e] = __builtin_amdgcn_exp2f(s[t][e] - from);
+        s[t][e] = __builtin_amdgcn_exp2f(minus(s[t][e], from));
         sum += s[t][e];
       }
     l = l * keep + sum;
@@ -944,6 +950,27 @@ __device__ __forceinline__ float max_halves(float x) {
 
 __device__ __forceinline__ void settle16(f32x16& a) { asm volatile("" : "+v"(a)); }
 
+// A weight's exponent is s scale - m in one operation, m the rounded product of
+// the largest s: off by m's rounding for all of a row alike, which the quotient
+// of the sums does not see, but which leaves every exponent's range where m is
+// past some 2^28.  Where a row of the wave has an m of 2^12 or more, the scores
+// are rounded first, so that the largest one's exponent is 0.  (A row below that
+// may have some tiles the one way and some the other: 2^-12 in the exponent, a
+// 20th of its weights' own rounding.)  Rows below it pay nothing: 16384 tokens x
+// 16 heads 1018 us with and without it (d = 128), 2250 and 2245 (256), 595 and 591
+// (64).
+constexpr float kFarScore = 0x1p12f;
+// What a row's largest score has to pass for its maximum to be looked at again:
+// 2^8 times the last one, whose weights lose nothing in fp32 or bf16; anything
+// where it is far.
+__device__ __forceinline__ float next_bar(float m) { return fabsf(m) >= kFarScore ? -INFINITY : m + 8.f; }
+__device__ __forceinline__ void scale_scores(f32x16 (&s)[2], float scale) {
+#pragma unroll
+  for (int n = 0; n < 32; ++n) s[n >> 4][n & 15] *= scale;
+  settle16(s[0]);  // (rounded here)
+  settle16(s[1]);
+}
+
 template <int D, bool PAGED, int GROUPS>
 __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kernel(AttnParams p, int tiles) {
   using H = PromptShape<D, GROUPS>;
@@ -980,7 +1007,7 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
   for (int i = 0; i < NC; ++i)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[i][e] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, bar = -INFINITY;
 
   // key tiles: those of the sinks, then those from the window's start on; a
   // group's are every GROUPS-th
@@ -1179,9 +1206,9 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
         float top = s[0][0];
 #pragma unroll
         for (int n = 1; n < 32; ++n) top = fmaxf(top, s[n >> 4][n & 15]);
-        // O and l are rescaled only where the maximum has grown by more than 2^8:
-        // weights of up to 2^8 lose nothing in fp32 or bf16
-        if (__any(top * scale > m + 8.f)) {
+        // O and l are rescaled only where the maximum has grown by more than 2^8
+        float by = scale;
+        if (__any(top * scale > bar)) {
           const float up = fmaxf(m, max_halves(top) * scale);
           const float keep = __builtin_amdgcn_exp2f(m - (up == -INFINITY ? 0.f : up));
           m = up;
@@ -1190,12 +1217,17 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
           for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[i][e] *= keep;
+          bar = next_bar(m);
+          if (__any(fabsf(m) >= kFarScore && m != -INFINITY)) {
+            scale_scores(s, scale);
+            by = 1.f;
+          }
         }
         const float base = m == -INFINITY ? 0.f : m;
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < 32; ++n) {
-          const float x = __builtin_amdgcn_exp2f(s[n >> 4][n & 15] * scale - base);
+          const float x = __builtin_amdgcn_exp2f(s[n >> 4][n & 15] * by - base);
           sum[n & 1] += x;
           w[n >> 3][n & 7] = (bf16)x;
         }
@@ -1220,7 +1252,7 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
           if (n < NK) a[n] = key(n % NS, n / NS);
           else if (n < NK + NV) a[n] = value((n - NK) / NC, (n - NK) % NC);
         };
-        float top[2], sum[2];
+        float top[2], sum[2], by = scale;
         const float before = m == -INFINITY ? 0.f : m;
         // The weights of the 16 scores of half b against a maximum, in steps of
         // `part`: a step forms exponents, the next one their powers, the one
@@ -1229,7 +1261,7 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
         const auto weigh = [&](int b, int step, int part, float base) __attribute__((always_inline)) {
 #pragma unroll
           for (int e = step * part; e < min(16, (step + 1) * part); ++e) {
-            y[e] = s[b][e] * scale - base;
+            y[e] = s[b][e] * by - base;
             if (b == 0) top[0] = e == 0 ? s[0][0] : fmaxf(top[0], s[0][e]);
           }
           if (step > 0) {
@@ -1266,10 +1298,9 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
         top[1] = s[1][0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top[1] = fmaxf(top[1], s[1][e]);
-        // O and l are rescaled only where the maximum has grown by more than 2^8:
-        // weights of up to 2^8 lose nothing in fp32 or bf16
+        // O and l are rescaled only where the maximum has grown by more than 2^8
         bool redo = false;  // (a flag: a branch over both would have O copied)
-        if (!whole || __any(fmaxf(top[0], top[1]) * scale > m + 8.f)) {
+        if (!whole || __any(fmaxf(top[0], top[1]) * scale > bar)) {
           top[0] = s[0][0];
 #pragma unroll
           for (int e = 1; e < 16; ++e) top[0] = fmaxf(top[0], s[0][e]);
@@ -1281,9 +1312,14 @@ __global__ __launch_bounds__(256 * GROUPS, (D == 256 ? 1 : 2)) void prompt_kerne
           for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[i][e] *= keep;
+          bar = next_bar(m);
           redo = true;
         }
         if (redo) {
+          if (__any(fabsf(m) >= kFarScore && m != -INFINITY)) {
+            scale_scores(s, scale);
+            by = 1.f;
+          }
 #pragma unroll
           for (int i = 0; i < 3; ++i) weigh(0, i, 16, m == -INFINITY ? 0.f : m);
         }

@@ -690,6 +690,7 @@ int gdn_cache_store(const gdn_tensor* k, const gdn_tensor* v, const gdn_tensor* 
  * sees none is 0.  Scores, the softmax's maximum and sum and the output are
  * held in fp32, and the output is rounded once; with bf16 inputs the weights
  * enter the product with v in bf16 (prompts: one term; single tokens: two).
+ * Scores may be of any size that fp32 holds (times log2 e).
  * Inputs of what is seen are expected to be finite: a NaN or infinity in a
  * key or value reaches the rows that see it and may reach earlier rows of its
  * own sequence in the same tile of 128 queries; none reaches another sequence,
