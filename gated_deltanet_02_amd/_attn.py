@@ -91,7 +91,8 @@ def gdn_cache_plan(ctx_lens, page_size: int, block_table, free_pages, n_free, cu
 
 def gdn_cache_release(done, seq_lens, page_size: int, block_table, free_pages, n_free, stream=None):
     """The pages of the requests with done[i] != 0 (int32) back onto the stack
-    free_pages[:n_free]; their lengths become 0.  All but ``done`` in place."""
+    free_pages[:n_free] (entries below 0 are none); their lengths become 0.
+    All but ``done`` in place."""
     L = _functions()
 
     def body(device, handle):

@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kLaunchMax = 1 << 23;  // workgroups of a launch (at most 256 threads each: 2^31)
 constexpr int kPlanThreads = 512;
+constexpr int kReleaseThreads = 1024;
 
 __device__ __forceinline__ int quotient(const Divide& d, int n) {
   return (int)((__umulhi(d.mul, (uint32_t)n) + (uint32_t)n) >> d.shift);
@@ -173,31 +174,99 @@ __global__ __launch_bounds__(kPlanThreads) void plan_finish_kernel(PlanParams p)
 }
 
 // The finished requests' pages back on the stack, in the order of the
-// requests; a round takes as many requests as there are threads.
-__global__ __launch_bounds__(kPlanThreads) void release_kernel(ReleaseParams p) {
-  __shared__ int64_t waves[kPlanThreads / 64];
-  __shared__ int64_t at[kPlanThreads];
-  __shared__ int count[kPlanThreads];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// requests; a round takes as many requests as there are threads, dealt out to
+// the waves, eight pieces of 64 entries at a time.  Entries below 0 name no page
+// and have no place on the stack: the pages are counted before any is written.
+// Bound by one workgroup's instructions and waits: 256 requests of 125 pages 13.8
+// us, 64 of 2048 18, 4096 of 13 126.
+__global__ __launch_bounds__(kReleaseThreads) void release_kernel(ReleaseParams p) {
+  constexpr int WAVES = kReleaseThreads / 64, BATCH = 8;
+  static_assert(WAVES * 64 == kReleaseThreads, "a row a lane");
+  __shared__ int64_t waves[WAVES], at_of[kReleaseThreads];
+  __shared__ int entries_of[kReleaseThreads];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int mine = wave + WAVES * lane;  // the lane's among the wave's requests
   int64_t top = min(max(p.n_free[0], 0), p.free_max);
-  for (int64_t i0 = 0; i0 < p.n; i0 += kPlanThreads) {
+  for (int64_t i0 = 0; i0 < p.n; i0 += kReleaseThreads) {
     const int64_t i = i0 + threadIdx.x;
-    int64_t pages = 0;
-    if (i < p.n && p.done[i]) pages = min(quotient_up(p.page, max(p.lens[i], 0)), p.width);
-    int64_t total;
-    const int64_t before = sums_before<kPlanThreads>(pages, waves, &total);
-    at[threadIdx.x] = top + before;
-    count[threadIdx.x] = (int)pages;
-    if (i < p.n && p.done[i]) p.lens[i] = 0;
-    __syncthreads();
-    for (int r = wave; r < kPlanThreads; r += kPlanThreads / 64) {
-      int32_t* row = p.table + (i0 + r) * p.table_st;
-      for (int j = lane; j < count[r]; j += 64) {
-        const int64_t to = at[r] + j;
-        if (to < p.free_max) p.free[to] = row[j];
-        row[j] = -1;
-      }
+    int entries = 0;
+    if (i < p.n && p.done[i]) {
+      entries = min(quotient_up(p.page, max(p.lens[i], 0)), p.width);
+      p.lens[i] = 0;
     }
+    entries_of[threadIdx.x] = entries;
+    __syncthreads();
+    entries = entries_of[mine];
+    const int over = entries % (64 * BATCH), whole = entries - over;
+    const uint64_t some = __ballot(over > 0);
+    int32_t* const rows = p.table + (i0 + wave) * p.table_st + lane;
+    const int64_t step = WAVES * p.table_st;
+    // what(the request's lane, entry, whether there is one, its address) for all
+    // pieces of the wave's requests: whole batches of a request, then what is
+    // over, of several requests a batch
+    const auto each = [&](const auto& what) {
+      int32_t e[BATCH];
+      for (uint64_t left = __ballot(whole > 0); left; left &= left - 1) {
+        const int k = __ffsll((unsigned long long)left) - 1, n = __builtin_amdgcn_readlane(whole, k);
+        int32_t* from = rows + k * step;
+        for (int j = 0; j < n; j += 64 * BATCH, from += 64 * BATCH) {
+#pragma unroll
+          for (int b = 0; b < BATCH; ++b) e[b] = from[64 * b];
+#pragma unroll
+          for (int b = 0; b < BATCH; ++b) what(k, e[b], true, from + 64 * b);
+        }
+      }
+      int k = 64, n = 0;
+      int32_t* from = nullptr;
+      uint64_t left = some;
+      const auto next = [&] {  // (k = 64: none)
+        k = left ? __ffsll((unsigned long long)left) - 1 : 64;
+        left &= left - 1;
+        n = k < 64 ? __builtin_amdgcn_readlane(over, k & 63) : 0;
+        from = rows + k * step + __builtin_amdgcn_readlane(whole, k & 63);
+      };
+      for (next(); k < 64;) {
+        int at[BATCH];
+        int32_t* place[BATCH];
+        bool is[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          at[b] = k;
+          place[b] = from;
+          is[b] = lane < n;
+          e[b] = is[b] ? *from : -1;
+          n -= 64;
+          from += 64;
+          if (n <= 0) next();
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) what(at[b], e[b], is[b], place[b]);
+      }
+    };
+    int pages = 0;
+    each([&](int k, int32_t e, bool, int32_t*) {
+      const int held = __popcll(__ballot(e >= 0));
+      pages += lane == k ? held : 0;
+    });
+    at_of[mine] = pages;
+    __syncthreads();
+    int64_t total;
+    const int64_t before = sums_before<kReleaseThreads>(at_of[threadIdx.x], waves, &total);
+    at_of[threadIdx.x] = top + before;
+    __syncthreads();
+    const int64_t first = at_of[mine];
+    int done = 0;  // of the lane's pages
+    each([&](int k, int32_t e, bool is, int32_t* place) {
+      const uint64_t held = __ballot(e >= 0);
+      const int64_t to = (((int64_t)__builtin_amdgcn_readlane((int)(first >> 32), k & 63) << 32) |
+                          (uint32_t)__builtin_amdgcn_readlane((int)first, k & 63)) +
+                         __builtin_amdgcn_readlane(done, k & 63) +
+                         (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(held >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)held, 0));
+      if (e >= 0 && to < p.free_max) p.free[to] = e;
+      if (is) *place = -1;
+      const int count = __popcll(held);
+      done += lane == k ? count : 0;
+    });
     __syncthreads();
     top += total;
   }
@@ -226,7 +295,7 @@ hipError_t launch_cache_plan(const PlanParams& p, hipStream_t s) {
 }
 
 hipError_t launch_cache_release(const ReleaseParams& p, hipStream_t s) {
-  hipLaunchKernelGGL(release_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+  hipLaunchKernelGGL(release_kernel, dim3(1), dim3(kReleaseThreads), 0, s, p);
   return hipGetLastError();
 }
 

@@ -660,8 +660,10 @@ int gdn_cache_plan(const gdn_tensor* ctx_lens, const gdn_tensor* cu_seqlens,
 /*
  * gdn_cache_release -- the pages of the requests with done[i] != 0 back onto
  * the stack, in the order of the requests and of their pages; their lengths
- * become 0 and their entries -1.  Pages past the end of free_pages [F] are
- * dropped.  A page belongs to one request.  done, seq_lens [N], block_table
+ * become 0 and their entries -1.  Entries below 0 name no page (one given up
+ * behind a window, say) and are passed over; any other is taken for a page of
+ * the cache.  Pages past the end of free_pages [F] are dropped.  A page belongs
+ * to one request.  done, seq_lens [N], block_table
  * [N, M], free_pages [F], n_free [1]: int32, the last four in place.
  */
 int gdn_cache_release(const gdn_tensor* done, gdn_tensor* seq_lens, gdn_tensor* block_table,

@@ -80,7 +80,7 @@ def release(done, lens, table, free, n_free: int, page: int):
         if not f:
             continue
         for j in range(min(-(-int(lens[i]) // page), table.shape[1])):
-            if n_free < len(free):
+            if table[i, j] >= 0 and n_free < len(free):
                 free[n_free] = table[i, j]
                 n_free += 1
             table[i, j] = -1
