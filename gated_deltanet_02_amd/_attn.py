@@ -54,6 +54,9 @@ def gdn_attn_default_options() -> GdnAttnOptions:
 
 
 def _options(scale, window, sinks):
+    """The packed options (0 is the C ABI's default scale, not a scale)."""
+    if scale == 0:
+        raise ValueError("scale must not be 0 (None for 1 / sqrt(d))")
     buf = (ctypes.c_char * _OPTIONS.size)()
     _OPTIONS.pack_into(buf, 0, 0.0 if scale is None else scale, window, sinks)
     return buf
@@ -124,16 +127,17 @@ def gdn_attn_prefill(q, k, v, cu_seqlens=None, block_table=None, seq_lens=None, 
     ``cu_seqlens``; k, v [T, Hk, d], or with ``block_table`` [N, M] and
     ``seq_lens`` [N] (int32) the caches, of whose sequences the queries are
     the last tokens.  With a ``window`` a query sees that many keys, its own
-    among them, and the first ``sinks``.  ``scale``: None for 1 / sqrt(d).
+    among them, and the first ``sinks``.  ``scale``: None for 1 / sqrt(d); 0
+    is refused.
     Returns out."""
     L = _functions()
+    o = _options(scale, window, sinks)
 
     def body(device, handle):
         y = _like(q) if out is None else out
         keep, pq, pk, pv, pc, pt, pl, po = _describe(device, (
             ("q", q), ("k", k), ("v", v), ("cu_seqlens", cu_seqlens), ("block_table", block_table),
             ("seq_lens", seq_lens), ("out", y)))
-        o = _options(scale, window, sinks)
         B._check(L.gdn_attn_prefill(pq, pk, pv, pc, pt, pl, po, ctypes.addressof(o), handle))
         return y
 
@@ -163,6 +167,7 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale: Optional[
     ``scale`` as ``gdn_attn_prefill``.  ``workspace``: a byte tensor from
     ``attn_workspace`` (allocated here if None).  Returns out [N, H, d]."""
     L = _functions()
+    o = _options(scale, window, sinks)
 
     def body(device, handle):
         y, ws = _like(q) if out is None else out, workspace
@@ -175,7 +180,6 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale: Optional[
             ws = torch.empty(n.value, dtype=torch.uint8, device=device)
         elif ws.dtype != torch.uint8 or not ws.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor")
-        o = _options(scale, window, sinks)
         B._check(L.gdn_attn_decode(pq, pk, pv, pt, pl, po, ctypes.addressof(o), ws.data_ptr(), ws.numel(), handle))
         return y
 

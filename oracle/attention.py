@@ -21,7 +21,7 @@ def attention(q, k, v, first: int, window: int = 0, sinks: int = 0, scale=None):
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     rows, H, d = q.shape
     n, Hk = k.shape[:2]
-    scale = d ** -0.5 if not scale else scale
+    scale = d ** -0.5 if scale is None else scale
     out, M, S = np.zeros((rows, H, d)), np.zeros((rows, H, d)), np.zeros((rows, H, 1))
     see = np.stack([seen(first + r, n, window, sinks) for r in range(rows)]) if rows else np.zeros((0, n), bool)
     any_seen = see.any(1)

@@ -1,0 +1,26 @@
+"""Arguments of the attention's binding that are refused before any tensor is
+looked at (no GPU needed)."""
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_02_amd as G
+from oracle import attention as A
+
+
+def test_a_scale_of_zero_is_refused():
+    """0 is how the C ABI names the default: it must not pass for one."""
+    x, c, t = torch.randn(4, 2, 64), torch.randn(3, 16, 2, 64), torch.zeros(4, 2, dtype=torch.int32)
+    for zero in (0, 0.0, -0.0):
+        with pytest.raises(ValueError, match="scale"):
+            G.gdn_attn_prefill(x, x, x, scale=zero)
+        with pytest.raises(ValueError, match="scale"):
+            G.gdn_attn_decode(x, c, c, t, t[:, 0].contiguous(), scale=zero)
+
+
+def test_the_reference_takes_a_scale_of_zero_as_it_is():
+    rng = np.random.default_rng(0)
+    q, k, v = (rng.standard_normal((5, 1, 4)) for _ in range(3))
+    out, _, _ = A.attention(q, k, v, 0, scale=0.0)
+    assert np.allclose(out[:, 0], [v[: i + 1, 0].mean(0) for i in range(5)])
+    assert not np.allclose(A.attention(q, k, v, 0)[0], out)
