@@ -62,6 +62,13 @@ def _options(scale, window, sinks):
     return buf
 
 
+def _page_size(n):
+    """A page size as the 32-bit argument it becomes (more bits would be cut)."""
+    if not 0 < n < 1 << 31:
+        raise ValueError(f"page_size must be 1 .. 2^31 - 1 (got {n})")
+    return n
+
+
 def gdn_cache_plan(ctx_lens, page_size: int, block_table, free_pages, n_free, cu_seqlens=None,
                    n_tokens: Optional[int] = None, seq_lens=None, slots=None, n_free_out=None, stream=None):
     """Block tables and slot maps from the requests' lengths: request i has
@@ -72,6 +79,7 @@ def gdn_cache_plan(ctx_lens, page_size: int, block_table, free_pages, n_free, cu
     where that is not given).  Returns (seq_lens [N] int32, slots [T] int64,
     n_free_out [1] int32); seq_lens may be ctx_lens and n_free_out n_free."""
     L = _functions()
+    page = _page_size(page_size)
 
     def body(device, handle):
         lens = torch.empty_like(ctx_lens) if seq_lens is None else seq_lens
@@ -86,7 +94,7 @@ def gdn_cache_plan(ctx_lens, page_size: int, block_table, free_pages, n_free, cu
             ("ctx_lens", ctx_lens), ("cu_seqlens", cu_seqlens), ("block_table", block_table),
             ("free_pages", free_pages), ("n_free", n_free), ("seq_lens", lens), ("slots", at),
             ("n_free_out", left)))
-        B._check(L.gdn_cache_plan(pc, pq, pt, pf, pn, page_size, pl, ps, po, handle))
+        B._check(L.gdn_cache_plan(pc, pq, pt, pf, pn, page, pl, ps, po, handle))
         return lens, at, left
 
     return _on(ctx_lens, stream, body)
@@ -97,12 +105,13 @@ def gdn_cache_release(done, seq_lens, page_size: int, block_table, free_pages, n
     free_pages[:n_free] (entries below 0 are none); their lengths become 0.
     All but ``done`` in place."""
     L = _functions()
+    page = _page_size(page_size)
 
     def body(device, handle):
         keep, pd, pl, pt, pf, pn = _describe(device, (
             ("done", done), ("seq_lens", seq_lens), ("block_table", block_table),
             ("free_pages", free_pages), ("n_free", n_free)))
-        B._check(L.gdn_cache_release(pd, pl, pt, pf, pn, page_size, handle))
+        B._check(L.gdn_cache_release(pd, pl, pt, pf, pn, page, handle))
 
     return _on(done, stream, body)
 

@@ -24,3 +24,12 @@ def test_the_reference_takes_a_scale_of_zero_as_it_is():
     out, _, _ = A.attention(q, k, v, 0, scale=0.0)
     assert np.allclose(out[:, 0], [v[: i + 1, 0].mean(0) for i in range(5)])
     assert not np.allclose(A.attention(q, k, v, 0)[0], out)
+
+
+@pytest.mark.parametrize("page", [0, -16, 2 ** 31, 2 ** 32 + 16, 2 ** 64])
+def test_page_sizes_of_more_than_32_bits_are_refused(page):
+    """2^32 + 16 must not pass for 16."""
+    i, t = torch.zeros(4, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: G.gdn_cache_plan(i, page, t, i, i[:1]), lambda: G.gdn_cache_release(i, i, page, t, i, i[:1])):
+        with pytest.raises(ValueError, match="page_size"):
+            call()
