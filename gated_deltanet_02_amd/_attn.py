@@ -63,9 +63,9 @@ def _options(scale, window, sinks):
 
 
 def _page_size(n):
-    """A page size as the 32-bit argument it becomes (more bits would be cut)."""
-    if not 0 < n < 1 << 31:
-        raise ValueError(f"page_size must be 1 .. 2^31 - 1 (got {n})")
+    """A page size that its 32-bit argument holds (more bits would be cut)."""
+    if not -1 << 31 <= n < 1 << 31:
+        raise ValueError(f"page_size: more than 32 bits ({n})")
     return n
 
 

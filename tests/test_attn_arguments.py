@@ -26,7 +26,7 @@ def test_the_reference_takes_a_scale_of_zero_as_it_is():
     assert not np.allclose(A.attention(q, k, v, 0)[0], out)
 
 
-@pytest.mark.parametrize("page", [0, -16, 2 ** 31, 2 ** 32 + 16, 2 ** 64])
+@pytest.mark.parametrize("page", [2 ** 31, 2 ** 32 + 16, -2 ** 32 + 16, 2 ** 64])
 def test_page_sizes_of_more_than_32_bits_are_refused(page):
     """2^32 + 16 must not pass for 16."""
     i, t = torch.zeros(4, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int32)
