@@ -77,7 +77,9 @@ def gdn_cache_plan(ctx_lens, page_size: int, block_table, free_pages, n_free, cu
     free_pages[:n_free], in ``block_table`` [N, M] (in place), all of them or
     none.  ``n_tokens``: the packed batch's tokens (the size of ``slots``
     where that is not given).  Returns (seq_lens [N] int32, slots [T] int64,
-    n_free_out [1] int32); seq_lens may be ctx_lens and n_free_out n_free."""
+    n_free_out [1] int32); seq_lens may be ctx_lens and n_free_out n_free.  A
+    request that gets no pages keeps its length, its tokens' slots are -1 and
+    their rows of the attention mean nothing: plan it again later."""
     L = _functions()
     page = _page_size(page_size)
 

@@ -647,7 +647,11 @@ int gdn_add_rms_norm(const gdn_tensor* x, const gdn_tensor* residual, const floa
  *   seq_lens     [N] int32: ctx + new, or ctx where a request got no pages
  *                (may be ctx_lens)
  *   slots        [T] int64: each new token's slot; -1 for those of a request
- *                that got no pages and those in no sequence
+ *                that got no pages and those in no sequence.  Nothing of such a
+ *                token is stored; its rows of the attention that follows mean
+ *                nothing (they are taken for the last tokens of the length that
+ *                stayed) and are left out by their slots, until a later plan
+ *                serves the request
  *   n_free_out   [1] int32: what is left on the stack (may be n_free)
  * ctx_lens [N], free_pages [F], n_free [1] are int32; all contiguous, the
  * table's row stride any.  A count n_free outside 0 .. F counts as those.
@@ -717,7 +721,8 @@ void gdn_attn_default_options(gdn_attn_options* opts);
  *               queries are the last tokens of the first seq_lens[i] that the
  *               cache holds of sequence i (the new ones stored already), so
  *               that a prompt can come in chunks or continue what is cached; a
- *               query before a sequence's first token sees none
+ *               query before a sequence's first token sees none.  Rows of a
+ *               request that gdn_cache_plan did not serve mean nothing
  *   block_table, seq_lens  [N, M], [N] int32, or both NULL
  *   opts        NULL for the defaults
  * d in {64, 128, 256}; unit stride in d, other strides multiples of 16 bytes;
@@ -732,7 +737,8 @@ int gdn_attn_prefill(const gdn_tensor* q, const gdn_tensor* k, const gdn_tensor*
 
 /*
  * gdn_attn_decode -- attention of one new token for each of N sequences, the
- * last of the seq_lens[i] that the cache holds (the new one stored already).
+ * last of the seq_lens[i] that the cache holds (the new one stored already;
+ * the row of a request that gdn_cache_plan did not serve means nothing).
  *   q, out     [N, H, d]; bf16 or f32
  *   workspace  gdn_attn_workspace_size() bytes of device memory, 256-byte
  *              aligned; not to be used by another call that overlaps on the
