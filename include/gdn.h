@@ -697,10 +697,12 @@ int gdn_cache_store(const gdn_tensor* k, const gdn_tensor* v, const gdn_tensor* 
  * held in fp32, and the output is rounded once; with bf16 inputs the weights
  * enter the product with v in bf16 (prompts: one term; single tokens: two).
  * Scores may be of any size that fp32 holds (times log2 e).
- * Inputs of what is seen are expected to be finite: a NaN or infinity in a
- * key or value reaches the rows that see it and may reach earlier rows of its
- * own sequence in the same tile of 128 queries; none reaches another sequence,
- * and what lies in the cache behind a sequence's length is never read.
+ * Inputs of what is seen are expected to be finite: a NaN or infinity in a key
+ * reaches the rows that see it and no others; one in a value these, and it may
+ * reach the other rows of their tiles of 128 queries (counted from a sequence's
+ * first query of the call), earlier ones and, with a window, later ones that no
+ * longer see it.  None reaches another sequence, and what lies in the cache
+ * behind a sequence's length is never read.
  */
 typedef struct gdn_attn_options {
   float scale;     /* multiplies the scores, within +-2^64; 0 (default):
