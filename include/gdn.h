@@ -728,7 +728,11 @@ void gdn_attn_default_options(gdn_attn_options* opts);
  *   block_table, seq_lens  [N, M], [N] int32, or both NULL
  *   opts        NULL for the defaults
  * d in {64, 128, 256}; unit stride in d, other strides multiples of 16 bytes;
- * tokens of k and v at most 2^24 elements apart.  The last bits of a result
+ * tokens of k and v at most 2^24 elements apart; at most 65535 query heads, and
+ * fewer than 2^23 (tile, head) pairs: tiles of 128 queries (f32: 64), T / 128
+ * and one for each sequence of a packed batch, those that a sequence fills
+ * without cu_seqlens (so 2^20 requests of a few tokens with 7 heads, or 2^17
+ * with 60; a larger batch in several calls).  The last bits of a result
  * depend on whether the call is large or small (keys are shared out between
  * more waves where tiles are few).
  */
@@ -741,7 +745,8 @@ int gdn_attn_prefill(const gdn_tensor* q, const gdn_tensor* k, const gdn_tensor*
  * gdn_attn_decode -- attention of one new token for each of N sequences, the
  * last of the seq_lens[i] that the cache holds (the new one stored already;
  * the row of a request that gdn_cache_plan did not serve means nothing).
- *   q, out     [N, H, d]; bf16 or f32
+ *   q, out     [N, H, d]; bf16 or f32; d in {64, 128, 256}, strides as
+ *              gdn_attn_prefill, at most 65535 query heads
  *   workspace  gdn_attn_workspace_size() bytes of device memory, 256-byte
  *              aligned; not to be used by another call that overlaps on the
  *              device.  It follows q's dtype and d alone
