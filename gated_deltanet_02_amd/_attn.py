@@ -54,8 +54,9 @@ def gdn_attn_default_options() -> GdnAttnOptions:
 
 
 def _options(scale, window, sinks):
-    """The packed options (0 is the C ABI's default scale, not a scale)."""
-    if scale == 0:
+    """The packed options (0, as a float, is the C ABI's default scale and not
+    a scale)."""
+    if scale is not None and ctypes.c_float(scale).value == 0:
         raise ValueError("scale must not be 0 (None for 1 / sqrt(d))")
     buf = (ctypes.c_char * _OPTIONS.size)()
     _OPTIONS.pack_into(buf, 0, 0.0 if scale is None else scale, window, sinks)

@@ -33,3 +33,12 @@ def test_page_sizes_of_more_than_32_bits_are_refused(page):
     for call in (lambda: G.gdn_cache_plan(i, page, t, i, i[:1]), lambda: G.gdn_cache_release(i, i, page, t, i, i[:1])):
         with pytest.raises(ValueError, match="page_size"):
             call()
+
+
+def test_a_scale_that_rounds_to_zero_is_refused():
+    x = torch.randn(4, 2, 64)
+    for tiny in (1e-46, -1e-300):
+        with pytest.raises(ValueError, match="scale"):
+            G.gdn_attn_prefill(x, x, x, scale=tiny)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        G.gdn_attn_prefill(x, x, x, scale=1e-44)
