@@ -691,9 +691,11 @@ hipError_t launch_step(AttnParams p, hipStream_t s) {
 
 // ---------------------------------------------------------------------------
 // prompts, f32: 16 queries a wave.  Either four waves share tiles of 32 keys for
-// 64 queries, or (SPLIT) they share 16 queries, each with every fourth tile.
-// Bound by fp32 matrix instructions: 4096 tokens x 16 heads 101 TFLOP/s with d =
-// 128, 96 with 64 and 99 with 256 (a product of 8192^3: 153).
+// 64 queries, or (SPLIT) four waves (d = 256: two) share 16 queries, each with
+// every fourth (second) tile, of 16 keys from d = 128 on.
+// Bound by fp32 matrix instructions and what stands between them: 4096 tokens x 16
+// heads 101 TFLOP/s with d = 128, 96 with 64 and 98 with 256 (a product of 8192^3:
+// 153).
 
 template <typename TI, int D, bool SPLIT>
 struct TileShape {
@@ -908,10 +910,11 @@ __global__ __launch_bounds__((64 * TileShape<TI, D, SPLIT>::NW)) void tile_kerne
 
 // ---------------------------------------------------------------------------
 // prompts, bf16: 32 queries a wave, tiles of 64 keys shared by four waves
-
 //
-// Bound by the matrix instructions: one prompt of 16384 tokens x 16 heads runs
-// at 1100 TFLOP/s with d = 128, 935 with 64 and 1020 with 256, where a product
+// Bound by products and softmax in turns, neither of which fills its unit (4096
+// tokens x 16 heads of 128: matrix cores busy 42 % of the time, the vector unit 43;
+// behind a cache with d = 256 37 and 34): one prompt of 16384 tokens x 16 heads
+// runs at 1117 TFLOP/s with d = 128, 948 with 64 and 1007 with 256, where a product
 // of 16384^3 reaches 1387.  32 columns a wave give 32 x 32 x 16 products whose
 // softmax is 16 scores a lane and 32 keys; at d <= 128 two waves a SIMD cover
 // each other's softmax (a third would not fit LDS and registers).  Weights of
@@ -1424,10 +1427,15 @@ hipError_t launch_prompt(const AttnParams& p, hipStream_t s) {
   const int tiles = (int)tiles_of(p, kPromptRows);
   // Few workgroups: the last one's time is the whole call's, and one that is
   // alone on its compute unit leaves half of it idle.  Measured, two groups and
-  // one, d = 128: one prompt of 4096 tokens x 16 heads (512 workgroups) 90 and 98
-  // us, 2048 x 16 35 and 43, 8192 x 8 143 and 170; of 4096 x 32 (1024) 157 and
-  // 152; with a window, whose tiles are alike, 2048 x 16 (256) 20.4 and 20.5,
-  // 8192 x 16 (1024) 76 and 58.
+  // one, d = 128 (64): one prompt of 4096 tokens x 16 heads (512 workgroups) 82 and
+  // 91 us (53 and 60), 2048 x 16 36 and 43 (24 and 31), 1024 x 16 21 and 24 (15 and
+  // 18), 8192 x 8 145 and 170 (96 and 112); past 512, 4096 x 20 110 and 100 (70 and
+  // 66), x 24 122 and 111, x 32 152 and 147.  With a window of 512, whose tiles are
+  // alike, 2048 x 16 (256) 18.5 and 20 (12.6 and 14.3), 4096 x 16 (512) 36 and 30 (23
+  // and 20), 8192 x 16 (1024) 69 and 55; of 128, 1024 x 16 12.8 and 11.5 (9 and 9).
+  // Workgroups count as the grid does, a packed batch's spare one a sequence and
+  // head too (4096 x 16 as a packed batch of one: 528), and any window as one that
+  // shortens chains, also one that is longer than the prompt.
   if constexpr (D <= 128)
     if ((int64_t)tiles * p.heads <= (p.window > 0 ? 256 : 512)) return launch_prompt<D, 2>(p, tiles, s);
   return launch_prompt<D, 1>(p, tiles, s);
@@ -1449,14 +1457,13 @@ template <typename TI, int D>
 hipError_t launch_tiles(const AttnParams& p, hipStream_t s) {
   // Few workgroups: keys shared out shorten the chain of tiles.  Measured,
   // split and not, d = 64, 8 heads: 256 tokens 9 and 18 us, 1024 26 and 57, 2048
-  // (256 workgroups) 78 and 111, 4096 266 and 259; with a window of 256, whose
-  // chains are short, 2048 40 and 25.
-  // Few workgroups: keys shared out shorten the chain of tiles.  Measured,
-  // split and not, d = 64, 8 heads: 256 tokens 9 and 18 us, 1024 26 and 57, 2048
-  // (256 workgroups) 78 and 111, 4096 266 and 259; with a window of 256, whose
-  // chains are short, 2048 40 and 25.  d = 256, two waves, one head: 3000 tokens
-  // 361 and 489, 8192 (128 workgroups) 1040 and 1311, two heads of that 2027 and
-  // 1313.
+  // (256 workgroups) 78 and 109, 4096 273 and 260; 16 heads, 1024 49 and 58, 2048
+  // 155 and 134.  d = 128, 8 heads: 256 13 and 28, 1024 43 and 97, 2048 142 and 187,
+  // 4096 522 and 462; 16 heads, 2048 282 and 235.  d = 256, two waves, one head:
+  // 1000 tokens 125 and 169, 3000 362 and 487, 8192 (128 workgroups) 1042 and 1311,
+  // two heads of that 2024 and 1318.  With a window of 256, 8 heads, 2048 40 and 23
+  // (d = 128 56 and 36), but 512 11.5 and 22 (16 and 35): the rule goes by the window's
+  // being there, not by the chains it leaves.
   if (p.window <= 0 && tiles_of(p, 64) * p.heads <= (D == 256 ? 128 : 256)) return launch_tiles<TI, D, true>(p, s);
   return launch_tiles<TI, D, false>(p, s);
 }
@@ -1471,9 +1478,7 @@ hipError_t launch_attn_prefill(bool bf16_in, int d, const AttnParams& p, hipStre
 }
 
 // One workgroup on each of 256 compute units.
-int attn_decode_waves(bool bf16_in, int d) {
-  return 256 * (bf16_in ? (d == 64 ? 8 : d == 128 ? 4 : 2) : (d == 64 ? 8 : d == 128 ? 4 : 2));
-}
+int attn_decode_waves(bool, int d) { return 256 * (d == 64 ? 8 : d == 128 ? 4 : 2); }
 hipError_t launch_attn_decode(bool bf16_in, int d, const AttnParams& p, hipStream_t s) {
   if (d == 64) return bf16_in ? launch_step<bf16, 64>(p, s) : launch_step<float, 64>(p, s);
   if (d == 128) return bf16_in ? launch_step<bf16, 128>(p, s) : launch_step<float, 128>(p, s);
